@@ -114,8 +114,12 @@ mxa_status_t prepare_decode(const void *q, const void *k_cache, const void *v_ca
   L.cu_q = nullptr;
   L.total_q = 0;
   L.out_f32 = 0;
+  L.window = L.sinks = 0;
   return MXA_OK;
 }
+
+// A sliding window of at least one key, with any number of sinks.
+bool valid_window(int window, int sinks) { return window >= 1 && sinks >= 0; }
 
 }  // namespace
 
@@ -318,6 +322,104 @@ mxa_status_t mxa_decode_fwd_varlen(const void *q, const int32_t *cu_seqlens_q, i
   L.cu_q = cu_seqlens_q;
   L.total_q = total_q;
   return launch_decode(L, static_cast<cudaStream_t>(stream));
+}
+
+mxa_status_t mxa_plan_window(const mxa_decode_params_t *p, int window, int sinks, int num_splits, int sm_count,
+                             mxa_plan_t *plan) {
+  if (p == nullptr || !valid_window(window, sinks)) return MXA_ERR_INVALID_ARG;
+  mxa_status_t st = check_shape(p);
+  if (st != MXA_OK) return st;
+  // a row streams the blocks of its window and sinks, however long it is
+  mxa_decode_params_t seen = *p;
+  seen.max_seqlen_k = (int)window_keys(*p, window, sinks);
+  return mxa_plan(&seen, num_splits, sm_count, plan);
+}
+
+mxa_status_t mxa_decode_fwd_window(const void *q, void *k_cache, void *v_cache, const void *k_new, const void *v_new,
+                                   const int32_t *block_table, const int32_t *cache_seqlens,
+                                   const mxa_decode_params_t *p, float scale, int window, int sinks,
+                                   const mxa_plan_t *plan, void *workspace, size_t workspace_bytes, void *out,
+                                   float *lse, void *stream) {
+  if (!valid_window(window, sinks) || (k_new == nullptr) != (v_new == nullptr)) return MXA_ERR_INVALID_ARG;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16)) return MXA_ERR_INVALID_ARG;
+  DecodeLaunch L;
+  mxa_status_t st = prepare_decode(q, k_cache, v_cache, block_table, cache_seqlens, p, scale, 1, plan, workspace,
+                                   workspace_bytes, out, lse, &L);
+  if (st != MXA_OK || p->B == 0) return st;
+  L.window = window;
+  L.sinks = sinks;
+  if (k_new != nullptr) {
+    L.len_add = p->q_len;
+    L.k_new = k_new;
+    L.v_new = v_new;
+  }
+  return launch_decode(L, static_cast<cudaStream_t>(stream));
+}
+
+mxa_status_t mxa_extend_tables(int32_t *block_table, const int32_t *cache_seqlens, const int32_t *cu_seqlens_q,
+                               const int32_t *free_pages, int B, int total_q, int num_free, int page_size,
+                               int num_pages, int max_pages_per_seq, int32_t *slots, int32_t *new_seqlens,
+                               int32_t *pages_used, void *stream) {
+  if (B < 0 || total_q < 0 || num_free < 0 || page_size < 1 || num_pages < 1 || max_pages_per_seq < 1)
+    return MXA_ERR_INVALID_ARG;
+  if (B == 0 && total_q > 0) return MXA_ERR_INVALID_ARG;
+  // slots, row capacities and the running page count are 32-bit
+  if ((long long)num_pages * page_size > INT32_MAX || (long long)max_pages_per_seq * page_size > INT32_MAX ||
+      (long long)B * max_pages_per_seq > INT32_MAX || total_q > INT32_MAX / 2 || B > INT32_MAX / 2)
+    return MXA_ERR_UNSUPPORTED;
+  if (pages_used == nullptr || !aligned(pages_used, 4)) return MXA_ERR_INVALID_ARG;
+  if (B > 0 && (block_table == nullptr || cache_seqlens == nullptr || cu_seqlens_q == nullptr || new_seqlens == nullptr))
+    return MXA_ERR_INVALID_ARG;
+  if ((num_free > 0 && free_pages == nullptr) || (total_q > 0 && slots == nullptr)) return MXA_ERR_INVALID_ARG;
+  for (const void *ptr : {(const void *)block_table, (const void *)cache_seqlens, (const void *)cu_seqlens_q,
+                          (const void *)free_pages, (const void *)slots, (const void *)new_seqlens})
+    if (!aligned(ptr, 4)) return MXA_ERR_INVALID_ARG;
+  if (B > 0 && new_seqlens == cache_seqlens) return MXA_ERR_INVALID_ARG;  // every CTA reads the old lengths
+  TableArgs a{};
+  a.block_table = block_table;
+  a.seqlens = cache_seqlens;
+  a.cu_q = cu_seqlens_q;
+  a.free_pages = free_pages;
+  a.slots = slots;
+  a.new_seqlens = new_seqlens;
+  a.pages_used = pages_used;
+  a.B = B;
+  a.total_q = total_q;
+  a.num_free = num_free;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  a.mpps = max_pages_per_seq;
+  return launch_extend_tables(a, static_cast<cudaStream_t>(stream));
+}
+
+mxa_status_t mxa_cache_write(const void *k_new, const void *v_new, long long k_token_stride, long long v_token_stride,
+                             const int32_t *slots, int total, int Hkv, int D, int num_pages, int page_size,
+                             mxa_dtype_t dtype, void *k_cache, void *v_cache, void *stream) {
+  if (total < 0 || Hkv < 1 || D < 1 || num_pages < 1 || page_size < 1) return MXA_ERR_INVALID_ARG;
+  if (dtype != MXA_F16 && dtype != MXA_BF16) return MXA_ERR_INVALID_ARG;
+  const long long row = (long long)Hkv * D;  // 16-bit values of a token
+  // 16-byte pieces; 32-bit slots
+  if (row % 8 != 0 || row > INT32_MAX || (long long)num_pages * page_size > INT32_MAX) return MXA_ERR_UNSUPPORTED;
+  if (k_token_stride % 8 != 0 || v_token_stride % 8 != 0) return MXA_ERR_UNSUPPORTED;
+  if (total > 0 && (k_token_stride < row || v_token_stride < row) && total > 1) return MXA_ERR_INVALID_ARG;
+  if (total == 0) return MXA_OK;
+  if (k_new == nullptr || v_new == nullptr || slots == nullptr || k_cache == nullptr || v_cache == nullptr)
+    return MXA_ERR_INVALID_ARG;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(slots, 4))
+    return MXA_ERR_INVALID_ARG;
+  WriteArgs a{};
+  a.k_new = static_cast<const uint4 *>(k_new);
+  a.v_new = static_cast<const uint4 *>(v_new);
+  a.k_stride = k_token_stride / 8;
+  a.v_stride = v_token_stride / 8;
+  a.k_cache = static_cast<uint4 *>(k_cache);
+  a.v_cache = static_cast<uint4 *>(v_cache);
+  a.slots = slots;
+  a.total = total;
+  a.chunks = (int)(row / 8);
+  a.pool_tokens = num_pages * page_size;
+  return launch_cache_write(a, static_cast<cudaStream_t>(stream));
 }
 
 mxa_status_t mxa_decode_fwd(const void *q, const void *k_cache, const void *v_cache,

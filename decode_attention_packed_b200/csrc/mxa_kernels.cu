@@ -172,17 +172,44 @@ __device__ __forceinline__ int tile_rows(const DecodeArgs &a, int qn, int rt) {
   return min(kRowsPerTile, qn * a.G - rt * kRowsPerTile);
 }
 
+// Blocks of a row that a sliding window leaves: with qn queries at positions
+// L - qn .. L - 1, the first of them sees keys >= low = L - qn + 1 - window,
+// and every query sees keys < sinks, so the keys in [sinks, low) are hidden
+// from the whole row.  The row's blocks are numbered without the hidden
+// ones: the first ns (sinks), then those from low's block on, which lie
+// `skip` further.  Without a window every block counts.
+struct RowSpan {
+  int nb, ns, skip;  // blocks left; those before the gap; blocks in the gap
+  int low;           // keys in [sinks, low) are hidden from every query
+  __device__ __forceinline__ int block(int v) const { return v < ns ? v : v + skip; }
+};
+template <int D, bool kWindow>
+__device__ __forceinline__ RowSpan row_span(const DecodeArgs &a, int L, int qn) {
+  constexpr int T = block_tokens(D);
+  RowSpan r;
+  r.nb = (L + T - 1) / T;
+  r.ns = r.skip = r.low = 0;
+  if constexpr (kWindow) {
+    const long long low = (long long)L - qn + 1 - a.window;
+    r.low = low > 0 ? (int)low : 0;
+    const int first = r.low / T;
+    r.ns = min((min(a.sinks, L) + T - 1) / T, first);
+    r.skip = first - r.ns;
+    r.nb -= r.skip;
+  }
+  return r;
+}
+
 // Index of the LSE of query t of row b (first packed token q0), head hq:
 // [B, Hq, q_len], or [Hq, total_q] with per-row offsets.
 __device__ __forceinline__ size_t lse_index(const DecodeArgs &a, int b, int q0, int hq, int t) {
   return a.cu_q != nullptr ? (size_t)hq * a.total_q + q0 + t : ((size_t)b * a.Hq + hq) * a.q_len + t;
 }
 
-template <int D, bool kVarlen>
+template <int D, bool kVarlen, bool kWindow>
 __device__ __forceinline__ void cursor_enter_row(Cursor &c, const DecodeArgs &a, int L) {
-  constexpr int T = block_tokens(D);
   c.L = L;
-  c.nb = (L + T - 1) / T;
+  c.nb = row_span<D, kWindow>(a, L, a.q_len).nb;
   if constexpr (kVarlen) {
     c.q0 = c.q0_next;
     c.qn = c.qn_next;
@@ -199,7 +226,7 @@ __device__ __forceinline__ void cursor_enter_row(Cursor &c, const DecodeArgs &a,
 
 // The segment at the cursor (a contiguous block range of one unit); the
 // cursor moves past it, and past the fixed cost of the unit that follows.
-template <int D, bool kVarlen>
+template <int D, bool kVarlen, bool kWindow>
 __device__ SegmentDesc cursor_take(Cursor &c, const DecodeArgs &a) {
   const int HR = a.Hkv * c.rtb;
   SegmentDesc s;
@@ -233,10 +260,10 @@ __device__ SegmentDesc cursor_take(Cursor &c, const DecodeArgs &a) {
       c.hr = 0;
       if (c.b + 1 < a.B) {
         ++c.b;
-        cursor_enter_row<D, kVarlen>(c, a, clamp_len(c.L_next, a.max_seqlen_k));
+        cursor_enter_row<D, kVarlen, kWindow>(c, a, clamp_len(c.L_next, a.max_seqlen_k));
         while (c.nb == 0 && c.b + 1 < a.B) {  // rows without keys (or queries) hold no units
           ++c.b;
-          cursor_enter_row<D, kVarlen>(c, a, clamp_len((long long)a.seqlens[c.b] + a.len_add, a.max_seqlen_k));
+          cursor_enter_row<D, kVarlen, kWindow>(c, a, clamp_len((long long)a.seqlens[c.b] + a.len_add, a.max_seqlen_k));
         }
         if (c.x + c.V >= c.end) c.end = c.x;  // that unit's first block lies past this range
       } else {
@@ -257,7 +284,7 @@ __device__ SegmentDesc cursor_take(Cursor &c, const DecodeArgs &a) {
 // row's tile count is its width over a unit's), and the row's own query
 // offsets are read again where a range starts.  UNIFORM: block range
 // [si * chunk, (si + 1) * chunk) of unit blockIdx.x / splits.
-template <int D, bool kVarlen>
+template <int D, bool kVarlen, bool kWindow>
 __device__ Cursor cursor_start(const DecodeArgs &a, uint8_t *smem, int lane, Cursor &tail, bool &has_tail) {
   constexpr int T = block_tokens(D);
   const int HR = a.Hkv * a.RT;
@@ -278,7 +305,7 @@ __device__ Cursor cursor_start(const DecodeArgs &a, uint8_t *smem, int lane, Cur
     c.hr = u % HR;
     row_queries<kVarlen>(a, c.b, c.q0, c.qn);
     c.L = clamp_len((long long)a.seqlens[c.b] + a.len_add, a.max_seqlen_k);
-    c.nb = (c.L + T - 1) / T;
+    c.nb = row_span<D, kWindow>(a, c.L, a.q_len).nb;
     if (kVarlen && c.hr % a.RT >= row_tiles(a, c.qn)) c.nb = 0;  // a tile past the row's queries
     const int beg = si * a.chunk_blocks, end = min(beg + a.chunk_blocks, c.nb);
     c.blk = beg;
@@ -295,7 +322,7 @@ __device__ Cursor cursor_start(const DecodeArgs &a, uint8_t *smem, int lane, Cur
   for (int i = lo; i < hi; ++i) {
     const int L = clamp_len((long long)a.seqlens[i] + a.len_add, a.max_seqlen_k);
     lens[i] = L;
-    const int nb = (L + T - 1) / T;
+    const int nb = row_span<D, kWindow>(a, L, a.q_len).nb;
     int w = nb > 0 ? nb + row_cost(a, i) : 0;  // positions of one unit of row i
     if constexpr (kVarlen) {      // times the row's tiles: one KV head's units
       int q0, qn;
@@ -414,9 +441,9 @@ __device__ __forceinline__ int bt_entry(const DecodeArgs &a, int b, int p, int n
 }
 
 // kAppend: the call appends new tokens to the cache (len_add > 0); kVarlen:
-// every row has its own query count (offsets cu_q).  The plain decode
-// instance carries none of that code.
-template <int D, bool kBf16, bool kAppend, bool kVarlen>
+// every row has its own query count (offsets cu_q); kWindow: a sliding window
+// with sinks.  The plain decode instance carries none of that code.
+template <int D, bool kBf16, bool kAppend, bool kVarlen, bool kWindow>
 __device__ void producer_warp(const TmapPair &tm, const DecodeArgs &a, uint8_t *smem, int lane) {
   constexpr int T = block_tokens(D);
   constexpr int CH = D / 64;
@@ -442,7 +469,7 @@ __device__ void producer_warp(const TmapPair &tm, const DecodeArgs &a, uint8_t *
   grid_dependency_wait();
   Cursor tail;
   bool has_tail;
-  Cursor cur = cursor_start<D, kVarlen>(a, smem, lane, tail, has_tail);
+  Cursor cur = cursor_start<D, kVarlen, kWindow>(a, smem, lane, tail, has_tail);
   auto more = [&]() { return has_tail || (cur.x < cur.end && cur.nb > 0); };
   // Publish the units of this CTA that are split across CTAs (at most the
   // first unit of its range and the tail unit): the epilogue warp tags their
@@ -464,9 +491,9 @@ __device__ void producer_warp(const TmapPair &tm, const DecodeArgs &a, uint8_t *
   auto take = [&]() {
     if (has_tail) {
       has_tail = false;
-      return cursor_take<D, kVarlen>(tail, a);
+      return cursor_take<D, kVarlen, kWindow>(tail, a);
     }
-    return cursor_take<D, kVarlen>(cur, a);
+    return cursor_take<D, kVarlen, kWindow>(cur, a);
   };
 
   // Publish a segment to the math warps: its descriptor and its Q tile.
@@ -490,7 +517,7 @@ __device__ void producer_warp(const TmapPair &tm, const DecodeArgs &a, uint8_t *
     w.base = 0;
     w.wa = w.wb = 0;
     if (a.contiguous) return;
-    w.base = (s.blk_beg * T) / ps;
+    w.base = (row_span<D, kWindow>(a, s.L, s.qn).block(s.blk_beg) * T) / ps;
     w.wa = bt_entry(a, s.b, w.base + lane, a.mpps);
     w.wb = bt_entry(a, s.b, w.base + 32 + lane, a.mpps);
   };
@@ -545,13 +572,19 @@ __device__ void producer_warp(const TmapPair &tm, const DecodeArgs &a, uint8_t *
       SegmentDesc nseg;
       Window nwin;
       int nnew0 = 0;
+      const RowSpan span = row_span<D, kWindow>(a, seg.L, seg.qn);
       for (int blk = seg.blk_beg; blk < seg.blk_end; ++blk) {
         const int s = it % kStages;
         const int k = it / kStages;
-        const int tok0 = blk * T;
+        const int tok0 = span.block(blk) * T;
         const int valid = min(T, seg.L - tok0);
         const int nbox = (valid + bt - 1) / bt;
         const int n_ops = nbox * CH * 2;  // one TMA box per (page box, 64-column chunk, K or V)
+        if (kWindow && !a.contiguous && tok0 / ps - win.base >= 64) {  // past the gap that the window leaves
+          win.base = tok0 / ps;
+          win.wa = bt_entry(a, seg.b, win.base + lane, a.mpps);
+          win.wb = bt_entry(a, seg.b, win.base + 32 + lane, a.mpps);
+        }
         if (!a.contiguous && tok0 / ps - win.base >= 32) {  // slide the window by 32 pages
           win.base += 32;
           win.wa = win.wb;
@@ -588,8 +621,11 @@ __device__ void producer_warp(const TmapPair &tm, const DecodeArgs &a, uint8_t *
             const int va = __shfl_sync(0xffffffffu, win.wa, src);
             const int vb = __shfl_sync(0xffffffffu, win.wb, src);
             page = idx < 32 ? va : vb;
-            if (page < 0 || page >= a.num_pages) {  // not a page of the pool: read as zeros, reported
-              bad_page |= op < n_ops;
+            // A box of hidden keys only is never read: its page may have gone
+            // back to the pool, or its table entry may hold anything.
+            const bool hidden = kWindow && tok >= a.sinks && tok + bt <= span.low;
+            if (hidden || page < 0 || page >= a.num_pages) {  // not a page of the pool: read as zeros, reported
+              bad_page |= !hidden && op < n_ops;
               page = -1;  // rows [-page_size, 0): outside the map, so the box is filled with zeros
             }
           }
@@ -685,7 +721,7 @@ __device__ __forceinline__ uint32_t handoff_addr(uint32_t sbase, int warp, int r
   return region + within + (chunk << 4) + ((uint32_t)(col & 3) << 2);
 }
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kWindow>
 __device__ void math_warps(const DecodeArgs &a, uint8_t *smem, int warp, int lane) {
   constexpr int T = block_tokens(D);
   constexpr int TW = T / kMathWarps;  // keys of one warp per stage
@@ -757,6 +793,14 @@ __device__ void math_warps(const DecodeArgs &a, uint8_t *smem, int warp, int lan
       if (r + 8 < rows) lim1 = min(L, L - qn + m1 / a.G + 1);
       tile_lim = min(L, L - qn + (rt * kRowsPerTile) / a.G + 1);
     }
+    // with a window (always causal) they are those from lim - window on, and the sinks
+    const RowSpan span = row_span<D, kWindow>(a, L, qn);
+    int low0 = 0, low1 = 0, tile_low = 0;
+    if constexpr (kWindow) {
+      low0 = lim0 - a.window;
+      low1 = lim1 - a.window;
+      tile_low = L - qn + (rt * kRowsPerTile + rows - 1) / a.G + 1 - a.window;
+    }
 
     float m_0 = NEG_INF, m_1 = NEG_INF, l_0 = 0.f, l_1 = 0.f;
     float o[DN][4];
@@ -770,15 +814,16 @@ __device__ void math_warps(const DecodeArgs &a, uint8_t *smem, int warp, int lan
       if (!warp_wait_bounded(bar_addr(smem, D, B_FULL(s)), k & 1, &g_mxa_err, kErrWaitFull, lane)) return;
       const uint32_t kbase = ring + (uint32_t)s * (2 * KV_BYTES);
       const uint32_t vbase = kbase + KV_BYTES;
-      const int j0 = blk * T + warp * TW;  // first key of this warp's slice
+      const int j0 = span.block(blk) * T + warp * TW;  // first key of this warp's slice
 
-      // Keys at or past L_b (page tail, unloaded boxes, stale data): their
-      // weights are 0, and their V rows are zeroed so that 0 * V stays 0.
-      if (j0 + TW > L) {
+      // Keys at or past L_b (page tail, unloaded boxes, stale data), and keys
+      // that a window hides from every query: their weights are 0, and their
+      // V rows are zeroed so that 0 * V stays 0.
+      if (j0 + TW > L || (kWindow && j0 < span.low && j0 + TW > a.sinks)) {
         for (int idx = lane; idx < TW * (D / 64) * 8; idx += 32) {
           const int jl = idx / ((D / 64) * 8);
           const int rem = idx % ((D / 64) * 8);
-          if (j0 + jl >= L) {
+          if (j0 + jl >= L || (kWindow && j0 + jl < span.low && j0 + jl >= a.sinks)) {
             const uint32_t addr = vbase + (uint32_t)(rem >> 3) * (T * 128) +
                                   (uint32_t)(warp * TW + jl) * 128 + (uint32_t)(rem & 7) * 16;
             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
@@ -808,7 +853,7 @@ __device__ void math_warps(const DecodeArgs &a, uint8_t *smem, int warp, int lan
       }
 
       // online softmax in the base-2 domain: x = s * scale * log2(e)
-      const bool need_mask = (j0 + TW > tile_lim);
+      const bool need_mask = (j0 + TW > tile_lim) || (kWindow && j0 < tile_low && j0 + TW > a.sinks);
       float mx0 = NEG_INF, mx1 = NEG_INF;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -817,8 +862,9 @@ __device__ void math_warps(const DecodeArgs &a, uint8_t *smem, int warp, int lan
           float x0 = sc[nt][e] * sl2, x1 = sc[nt][2 + e] * sl2;
           if (need_mask) {
             const int jj = j0 + nt * 8 + 2 * c + e;
-            x0 = jj < lim0 ? x0 : NEG_INF;
-            x1 = jj < lim1 ? x1 : NEG_INF;
+            const bool sink = kWindow && jj < a.sinks;
+            x0 = jj < lim0 && (!kWindow || sink || jj >= low0) ? x0 : NEG_INF;
+            x1 = jj < lim1 && (!kWindow || sink || jj >= low1) ? x1 : NEG_INF;
           }
           sc[nt][e] = x0;
           sc[nt][2 + e] = x1;
@@ -1500,7 +1546,7 @@ __device__ void epilogue_warp(const DecodeArgs &a, uint8_t *smem, int lane) {
 // ---------------------------------------------------------------------------
 // The split kernel
 // ---------------------------------------------------------------------------
-template <int D, bool kBf16, bool kAppend, bool kVarlen>
+template <int D, bool kBf16, bool kAppend, bool kVarlen, bool kWindow>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
     mxa_split_kernel(const __grid_constant__ TmapPair tm, const __grid_constant__ DecodeArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -1533,11 +1579,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
   // warps).  The math warps touch shared memory only.
   grid_launch_dependents();
   if (warp == kProducerWarp) {
-    producer_warp<D, kBf16, kAppend, kVarlen>(tm, a, smem, lane);
+    producer_warp<D, kBf16, kAppend, kVarlen, kWindow>(tm, a, smem, lane);
   } else if (warp == kEpilogueWarp) {
     epilogue_warp<D, kBf16>(a, smem, lane);
   } else {
-    math_warps<D, kBf16>(a, smem, warp, lane);
+    math_warps<D, kBf16, kWindow>(a, smem, warp, lane);
   }
 }
 
@@ -1670,13 +1716,13 @@ bool kv_maps(TmapPair *tm, const void *k, const void *v, int D, int Hkv, long lo
   return true;
 }
 
-template <int D, bool kBf16, bool kAppend, bool kVarlen>
+template <int D, bool kBf16, bool kAppend, bool kVarlen, bool kWindow>
 cudaError_t prepare_split_kernel(int device) {
   static std::mutex mu;
   static bool done[kMaxDevices] = {};
   std::lock_guard<std::mutex> lock(mu);
   if (device >= 0 && device < kMaxDevices && done[device]) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(mxa_split_kernel<D, kBf16, kAppend, kVarlen>,
+  cudaError_t e = cudaFuncSetAttribute(mxa_split_kernel<D, kBf16, kAppend, kVarlen, kWindow>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_total(D));
   if (e == cudaSuccess && device >= 0 && device < kMaxDevices) done[device] = true;
   return e;
@@ -1697,12 +1743,8 @@ mxa_status_t launch_typed(const DecodeLaunch &L, cudaStream_t stream) {
   const mxa_plan_t &plan = L.plan;
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return MXA_ERR_CUDA;
-  const bool append = L.len_add > 0, varlen = L.cu_q != nullptr;
-  if (append && varlen) return MXA_ERR_UNSUPPORTED;
-  const cudaError_t pe = append   ? prepare_split_kernel<D, kBf16, true, false>(device)
-                         : varlen ? prepare_split_kernel<D, kBf16, false, true>(device)
-                                  : prepare_split_kernel<D, kBf16, false, false>(device);
-  if (pe != cudaSuccess) return MXA_ERR_CUDA;
+  const bool append = L.len_add > 0, varlen = L.cu_q != nullptr, window = L.window > 0;
+  if (varlen && (append || window)) return MXA_ERR_UNSUPPORTED;
 
   DecodeArgs a{};
   a.q = L.q;
@@ -1729,7 +1771,9 @@ mxa_status_t launch_typed(const DecodeLaunch &L, cudaStream_t stream) {
   a.causal = L.causal;
   a.schedule = plan.schedule;
   a.splits = plan.num_splits;
-  const int max_blocks = (p.max_seqlen_k + T - 1) / T;
+  a.window = L.window;
+  a.sinks = L.sinks;
+  const int max_blocks = (int)(((window ? window_keys(p, L.window, L.sinks) : p.max_seqlen_k) + T - 1) / T);
   a.chunk_blocks = plan.schedule == MXA_SCHED_UNIFORM ? (max_blocks + plan.num_splits - 1) / plan.num_splits : 1;
   if (a.chunk_blocks < 1) a.chunk_blocks = 1;
   a.units = plan.units;
@@ -1762,9 +1806,18 @@ mxa_status_t launch_typed(const DecodeLaunch &L, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = append   ? cudaLaunchKernelEx(&cfg, mxa_split_kernel<D, kBf16, true, false>, tm, a)
-                        : varlen ? cudaLaunchKernelEx(&cfg, mxa_split_kernel<D, kBf16, false, true>, tm, a)
-                                 : cudaLaunchKernelEx(&cfg, mxa_split_kernel<D, kBf16, false, false>, tm, a);
+  auto launch = [&](auto ap, auto vl, auto wd) -> cudaError_t {
+    constexpr bool A = decltype(ap)::value, V = decltype(vl)::value, W = decltype(wd)::value;
+    const cudaError_t pe = prepare_split_kernel<D, kBf16, A, V, W>(device);
+    return pe != cudaSuccess ? pe : cudaLaunchKernelEx(&cfg, mxa_split_kernel<D, kBf16, A, V, W>, tm, a);
+  };
+  using std::false_type;
+  using std::true_type;
+  const cudaError_t e = window ? (append ? launch(true_type{}, false_type{}, true_type{})
+                                         : launch(false_type{}, false_type{}, true_type{}))
+                        : append ? launch(true_type{}, false_type{}, false_type{})
+                        : varlen ? launch(false_type{}, true_type{}, false_type{})
+                                 : launch(false_type{}, false_type{}, false_type{});
   if (e != cudaSuccess) return MXA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MXA_OK : MXA_ERR_CUDA;
 }
@@ -1790,6 +1843,24 @@ mxa_status_t launch_combine(const float *o_part, const float *lse_part, int num_
   else
     mxa_combine_kernel<false><<<blocks, 128, 0, stream>>>(o_part, lse_part, num_splits, B, q_len, Hq, D, out, lse);
   return cudaGetLastError() == cudaSuccess ? MXA_OK : MXA_ERR_CUDA;
+}
+
+mxa_status_t device_error_word(int **word) {
+  static std::mutex mu;
+  static int *cache[kMaxDevices] = {};
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return MXA_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(mu);
+  const bool known = device >= 0 && device < kMaxDevices;
+  if (known && cache[device] != nullptr) {
+    *word = cache[device];
+    return MXA_OK;
+  }
+  void *p = nullptr;
+  if (cudaGetSymbolAddress(&p, g_mxa_err) != cudaSuccess) return MXA_ERR_CUDA;
+  if (known) cache[device] = static_cast<int *>(p);
+  *word = static_cast<int *>(p);
+  return MXA_OK;
 }
 
 mxa_status_t read_device_error(int reset, int *flags) {

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "mxa.h"
+#include "mxa_config.h"
 
 namespace mxa {
 
@@ -49,6 +50,7 @@ struct DecodeArgs {
   uint16_t *v_cache_w;
   unsigned int epoch;          // tags this launch's arrival counts
   int out_f32;                 // 1: out holds float32 (the value before its one rounding)
+  int window, sinks;           // sliding window (0: none): query at p sees keys in (p - window, p] and keys < sinks
 };
 
 // Everything launch_decode needs; pointers are device pointers.
@@ -67,15 +69,52 @@ struct DecodeLaunch {
   const int32_t *cu_q;        // varlen: [B + 1] query offsets (null: q_len queries per row)
   int total_q;                // varlen: packed query tokens
   int out_f32;                // out is float32 instead of the input type
+  int window, sinks;          // sliding window (0: none) and the first keys that stay visible
 };
+
+// Upper bound on the keys in the blocks that a windowed row of `p` streams:
+// its sinks and its window, each widened to whole blocks.
+inline long long window_keys(const mxa_decode_params_t &p, int window, int sinks) {
+  const long long keys = (long long)window + p.q_len - 1 + sinks + 3LL * block_tokens(p.D);
+  return keys < p.max_seqlen_k ? keys : p.max_seqlen_k;
+}
 
 // Launch the split kernel (split units are merged inside it).
 mxa_status_t launch_decode(const DecodeLaunch &L, cudaStream_t stream);
+
+// Pages and slots for a step's new tokens (mxa_extend_tables).
+struct TableArgs {
+  int32_t *block_table;         // [B, mpps]
+  const int32_t *seqlens;       // [B] keys held before the step
+  const int32_t *cu_q;          // [B + 1] offsets of each row's new tokens
+  const int32_t *free_pages;    // [num_free]
+  int32_t *slots;               // [total_q]
+  int32_t *new_seqlens;         // [B]
+  int32_t *pages_used;          // [1]
+  int B, total_q, num_free, page_size, num_pages, mpps;
+  int *err;
+};
+mxa_status_t launch_extend_tables(TableArgs a, cudaStream_t stream);
+
+// New keys and values into their slots (mxa_cache_write).
+struct WriteArgs {
+  const uint4 *k_new, *v_new;   // [total][chunks], tokens k_stride / v_stride pieces apart
+  long long k_stride, v_stride;
+  uint4 *k_cache, *v_cache;     // [pool_tokens][chunks]
+  const int32_t *slots;         // [total]
+  int total, chunks, pool_tokens;
+  int *err;
+};
+mxa_status_t launch_cache_write(WriteArgs a, cudaStream_t stream);
 
 // Launch the uniform-layout combine of mxa_combine().
 mxa_status_t launch_combine(const float *o_part, const float *lse_part, int num_splits, int B,
                             int q_len, int Hq, int D, mxa_dtype_t dtype, void *out, float *lse,
                             cudaStream_t stream);
+
+// Address of the current device's failure record, for kernels outside the
+// translation unit that defines it (looked up once per device).
+mxa_status_t device_error_word(int **word);
 
 // Read (and optionally clear) the device-side failure record of the current device.
 mxa_status_t read_device_error(int reset, int *flags);

@@ -31,7 +31,8 @@ EXPORTED = ("mxa_status_string", "mxa_should_pack_gqa", "mxa_num_splits_heuristi
             "mxa_plan_balanced",
             "mxa_decode_fwd", "mxa_decode_fwd_with_plan", "mxa_combine", "mxa_device_error",
             "mxa_decode_fwd_noalloc", "mxa_decode_fwd_append", "mxa_decode_fwd_varlen",
-            "mxa_decode_fwd_f32out", "mxa_decode_workspace_size")
+            "mxa_decode_fwd_f32out", "mxa_decode_workspace_size", "mxa_plan_window", "mxa_decode_fwd_window",
+            "mxa_extend_tables", "mxa_cache_write")
 
 SIZE_MAX = ctypes.c_size_t(-1).value
 
@@ -88,6 +89,16 @@ _lib.mxa_decode_fwd_varlen.restype = _I
 _lib.mxa_decode_fwd_noalloc.argtypes = [_P, _P, _P, _P, _P, ctypes.POINTER(mxa_decode_params_t),
                                         ctypes.c_float, _I, _I, _P, _P, _P]
 _lib.mxa_decode_fwd_noalloc.restype = _I
+_lib.mxa_plan_window.argtypes = [ctypes.POINTER(mxa_decode_params_t), _I, _I, _I, _I, ctypes.POINTER(mxa_plan_t)]
+_lib.mxa_plan_window.restype = _I
+_lib.mxa_decode_fwd_window.argtypes = [_P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(mxa_decode_params_t),
+                                       ctypes.c_float, _I, _I, ctypes.POINTER(mxa_plan_t), _P, ctypes.c_size_t,
+                                       _P, _P, _P]
+_lib.mxa_decode_fwd_window.restype = _I
+_lib.mxa_extend_tables.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P]
+_lib.mxa_extend_tables.restype = _I
+_lib.mxa_cache_write.argtypes = [_P, _P, ctypes.c_longlong, ctypes.c_longlong, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P]
+_lib.mxa_cache_write.restype = _I
 _lib.mxa_combine.argtypes = [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P]
 _lib.mxa_combine.restype = _I
 _lib.mxa_device_error.argtypes = [_I]
@@ -219,6 +230,48 @@ def mxa_decode_fwd_noalloc(q, k_cache, v_cache, block_table, cache_seqlens, para
                                        _stream(stream)), "mxa_decode_fwd_noalloc")
 
 
+def mxa_plan_window(params: mxa_decode_params_t, window: int, sinks: int = 0, num_splits: int = 0,
+                    sm_count: int = 0) -> mxa_plan_t:
+    plan = mxa_plan_t()
+    _check(_lib.mxa_plan_window(ctypes.byref(params), int(window), int(sinks), num_splits, sm_count,
+                                ctypes.byref(plan)), "mxa_plan_window")
+    return plan
+
+
+def mxa_decode_fwd_window(q, k_cache, v_cache, k_new, v_new, block_table, cache_seqlens, params, scale, window,
+                          sinks, plan, workspace, out, lse, stream=None) -> None:
+    """Causal decode in which the query at position p sees its last `window`
+    keys and the first `sinks` keys; k_new / v_new as in
+    mxa_decode_fwd_append, or None (see mxa.h)."""
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.mxa_decode_fwd_window(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_new), _ptr(v_new),
+                                      _ptr(block_table), _ptr(cache_seqlens), ctypes.byref(params), float(scale),
+                                      int(window), int(sinks), ctypes.byref(plan), _ptr(workspace), ws_bytes,
+                                      _ptr(out), _ptr(lse), _stream(stream)), "mxa_decode_fwd_window")
+
+
+def mxa_extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, page_size, num_pages, slots,
+                      new_seqlens, pages_used, stream=None) -> None:
+    """Pages from the front of free_pages for the step's new tokens, written
+    into block_table [B, width], and every new token's cache slot (see mxa.h)."""
+    B, width = block_table.shape
+    _check(_lib.mxa_extend_tables(_ptr(block_table), _ptr(cache_seqlens), _ptr(cu_seqlens_q), _ptr(free_pages), B,
+                                  slots.numel(), free_pages.numel(), int(page_size), int(num_pages), width,
+                                  _ptr(slots), _ptr(new_seqlens), _ptr(pages_used), _stream(stream)),
+           "mxa_extend_tables")
+
+
+def mxa_cache_write(k_new, v_new, slots, k_cache, v_cache, stream=None) -> None:
+    """k_cache / v_cache [num_pages, page_size, Hkv, D] at slots[t] become
+    k_new / v_new [total, Hkv, D] (tokens may be strided; see mxa.h)."""
+    total, Hkv, D = k_new.shape
+    num_pages, page_size = k_cache.shape[:2]
+    dtype = MXA_BF16 if k_cache.dtype == torch.bfloat16 else MXA_F16
+    ks, vs = (k_new.stride(0), v_new.stride(0)) if total > 1 else (Hkv * D, Hkv * D)
+    _check(_lib.mxa_cache_write(_ptr(k_new), _ptr(v_new), ks, vs, _ptr(slots), total, Hkv, D, num_pages, page_size,
+                                dtype, _ptr(k_cache), _ptr(v_cache), _stream(stream)), "mxa_cache_write")
+
+
 def mxa_combine(o_part, lse_part, out, lse=None, stream=None) -> None:
     """o_part [S, B, q_len, Hq, D] fp32, lse_part [S, B, Hq, q_len] fp32 -> out [B, q_len, Hq, D]."""
     S, B, q_len, Hq, D = o_part.shape
@@ -268,10 +321,10 @@ class Prepared:
 
 
 def prepare(q, k_cache, block_table, *, max_seqlen_k=None, num_splits=0, plan=None,
-            device=None) -> Prepared:
+            device=None, window=0, sinks=0) -> Prepared:
     params = params_for(q, k_cache, block_table, max_seqlen_k)
     if plan is None:
-        plan = mxa_plan(params, num_splits)
+        plan = mxa_plan_window(params, window, sinks, num_splits) if window else mxa_plan(params, num_splits)
     ws = None
     if plan.workspace_bytes:
         ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=device or q.device)
@@ -280,18 +333,27 @@ def prepare(q, k_cache, block_table, *, max_seqlen_k=None, num_splits=0, plan=No
 
 def decode(q, k_cache, v_cache, block_table, cache_seqlens, *, scale=None, causal=False,
            num_splits=0, max_seqlen_k=None, out=None, lse=None, prepared: Optional[Prepared] = None,
-           return_lse=True, stream=None, k_new=None, v_new=None, out_dtype=None):
+           return_lse=True, stream=None, k_new=None, v_new=None, out_dtype=None, window=0, sinks=0):
     """out [B, q_len, Hq, D] (and lse [B, Hq, q_len] fp32) for one decode step.
 
     With k_new / v_new [B, q_len, Hkv, D] the step first writes them into the
     cache at positions cache_seqlens[b] + t and attends to cache_seqlens[b] +
     q_len keys; max_seqlen_k must then bound those lengths.  out_dtype =
     torch.float32 returns O before its rounding to q's type
-    (mxa_decode_fwd_f32out)."""
+    (mxa_decode_fwd_f32out).
+
+    window > 0 (causal only) leaves each query its last `window` keys and the
+    first `sinks` keys of its row (mxa_decode_fwd_window); the blocks between
+    them are not read."""
+    if window < 0 or sinks < 0 or (sinks and not window):
+        raise ValueError("window >= 0, and sinks >= 0 go with a window")
+    if window and not causal:
+        raise ValueError("a sliding window is causal: pass causal=True")
     if scale is None:
         scale = q.shape[-1] ** -0.5
     if prepared is None:
-        prepared = prepare(q, k_cache, block_table, max_seqlen_k=max_seqlen_k, num_splits=num_splits)
+        prepared = prepare(q, k_cache, block_table, max_seqlen_k=max_seqlen_k, num_splits=num_splits,
+                           window=window, sinks=sinks)
     f32 = out_dtype == torch.float32 or (out is not None and out.dtype == torch.float32)
     if out is None:
         out = torch.empty(q.shape, dtype=torch.float32, device=q.device) if f32 else torch.empty_like(q)
@@ -301,10 +363,15 @@ def decode(q, k_cache, v_cache, block_table, cache_seqlens, *, scale=None, causa
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new go together")
     if f32:
+        if window:
+            raise ValueError("a float32 output is not offered with a window")
         if k_new is not None:
             raise ValueError("a float32 output is not offered with k_new / v_new")
         mxa_decode_fwd_f32out(q, k_cache, v_cache, block_table, cache_seqlens, prepared.params, scale, causal,
                               prepared.plan, prepared.workspace, out, lse, stream)
+    elif window:
+        mxa_decode_fwd_window(q, k_cache, v_cache, k_new, v_new, block_table, cache_seqlens, prepared.params, scale,
+                              window, sinks, prepared.plan, prepared.workspace, out, lse, stream)
     elif k_new is None:
         mxa_decode_fwd_with_plan(q, k_cache, v_cache, block_table, cache_seqlens, prepared.params, scale,
                                  causal, prepared.plan, prepared.workspace, out, lse, stream)
@@ -340,3 +407,77 @@ def decode_varlen(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens,
     mxa_decode_fwd_varlen(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, prepared.params,
                           scale, causal, prepared.plan, prepared.workspace, out, lse, stream)
     return out, lse
+
+
+# --------------------------------------------------------------------------
+# the cache's bookkeeping
+# --------------------------------------------------------------------------
+
+def _want_here(t: torch.Tensor, name: str) -> None:
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+
+
+def _want(t: torch.Tensor, name: str, dtype, shape=None) -> None:
+    """A dense tensor of `dtype` (and `shape`) on the current device, or an error that names it."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    _want_here(t, name)
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, *, page_size, num_pages, total_q,
+                  slots=None, new_seqlens=None, pages_used=None, stream=None):
+    """Pages and cache slots for a step's new tokens: row b holds
+    cache_seqlens[b] keys and receives cu_seqlens_q[b + 1] - cu_seqlens_q[b]
+    tokens, total_q in all.  The pages it needs besides those it holds are
+    taken from the front of free_pages, in row order, and written into
+    block_table [B, width] (all int32, on the device).
+
+    Returns (slots [total_q], new_seqlens [B], pages_used [1]), int32.  A row
+    whose pages do not fit its table or the free list takes none: its slots
+    are -1 and its length is unchanged."""
+    _want(block_table, "block_table", torch.int32)
+    B = block_table.shape[0]
+    dev = block_table.device
+    _want(cache_seqlens, "cache_seqlens", torch.int32, (B,))
+    _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
+    _want(free_pages, "free_pages", torch.int32)
+    if slots is None:
+        slots = torch.empty(total_q, dtype=torch.int32, device=dev)
+    if new_seqlens is None:
+        new_seqlens = torch.empty(B, dtype=torch.int32, device=dev)
+    if pages_used is None:
+        pages_used = torch.empty(1, dtype=torch.int32, device=dev)
+    _want(slots, "slots", torch.int32, (total_q,))
+    _want(new_seqlens, "new_seqlens", torch.int32, (B,))
+    _want(pages_used, "pages_used", torch.int32, (1,))
+    if B and new_seqlens.data_ptr() == cache_seqlens.data_ptr():
+        raise ValueError("new_seqlens must be another buffer than cache_seqlens")
+    mxa_extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, page_size, num_pages, slots,
+                      new_seqlens, pages_used, stream)
+    return slots, new_seqlens, pages_used
+
+
+def write_cache(k_new, v_new, k_cache, v_cache, slots, *, stream=None) -> None:
+    """Copy k_new / v_new [total, Hkv, D] into the cache slots of
+    extend_tables.  The tokens may be strided (slices of one fused
+    projection); a token with slot -1 is left out; slots are distinct."""
+    _want(k_cache, "k_cache", k_cache.dtype)
+    _want(v_cache, "v_cache", k_cache.dtype, k_cache.shape)
+    if k_cache.dtype is not torch.bfloat16 and k_cache.dtype is not torch.float16:
+        raise TypeError("the cache must be float16 or bfloat16")
+    total, Hkv, D = k_new.shape
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if t.dtype is not k_cache.dtype:
+            raise TypeError(f"{name} must have the cache's type")
+        _want_here(t, name)
+        if t.shape != (total,) + k_cache.shape[2:]:
+            raise ValueError(f"{name} must be [total, Hkv, D] with the cache's heads")
+        if total and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != D)):
+            raise ValueError(f"a token of {name} must be contiguous")
+    _want(slots, "slots", torch.int32, (total,))
+    mxa_cache_write(k_new, v_new, slots, k_cache, v_cache, stream)

@@ -275,6 +275,86 @@ MXA_API mxa_status_t mxa_decode_fwd_append(const void *q, void *k_cache, void *v
                                            float scale, int causal, const mxa_plan_t *plan, void *workspace,
                                            size_t workspace_bytes, void *out, float *lse, void *stream);
 
+/* mxa_plan for a call with a sliding window (mxa_decode_fwd_window): a row
+ * streams at most the blocks of its window and its sinks, so a long row is
+ * not cut into more pieces than those blocks fill.  window >= 1, sinks >= 0.
+ * Arguments and errors otherwise as mxa_plan. */
+MXA_API mxa_status_t mxa_plan_window(const mxa_decode_params_t *params, int window, int sinks, int num_splits,
+                                     int sm_count, mxa_plan_t *plan);
+
+/* Causal decode attention with a sliding window and sinks: the query at
+ * position p (query t of row b is at p = L_b - q_len + t) sees the keys
+ *   j <= p  with  j > p - window  or  j < sinks,
+ * that is its last `window` keys, itself among them, and the first `sinks`
+ * keys of the row.  The softmax runs over exactly these keys; blocks of keys
+ * that no query of the row sees are not read, and neither is a page that
+ * holds such keys only (its block-table entry may hold anything), so a caller
+ * may give the pages between the sinks and the window back to its pool.
+ *   window : >= 1; a window of max_seqlen_k or more is plain causal attention
+ *   sinks  : >= 0
+ *   k_new, v_new : as in mxa_decode_fwd_append (the step's tokens are written
+ *            into the cache first and L_b grows by q_len), or both NULL: the
+ *            cache then holds them already and is not written
+ *   plan   : mxa_plan_window's (any plan valid for `params` may be used)
+ * Other arguments and errors as mxa_decode_fwd_with_plan (and, with k_new,
+ * mxa_decode_fwd_append). */
+MXA_API mxa_status_t mxa_decode_fwd_window(const void *q, void *k_cache, void *v_cache, const void *k_new,
+                                           const void *v_new, const int32_t *block_table,
+                                           const int32_t *cache_seqlens, const mxa_decode_params_t *params,
+                                           float scale, int window, int sinks, const mxa_plan_t *plan,
+                                           void *workspace, size_t workspace_bytes, void *out, float *lse,
+                                           void *stream);
+
+/* Pages and cache slots for a step's new tokens, on the device: row b holds
+ * L_b keys in its first ceil(L_b / page_size) pages and receives
+ * n_b = cu_seqlens_q[b + 1] - cu_seqlens_q[b] new tokens.
+ *   block_table  : device [B, max_pages_per_seq]: the pages each row needs
+ *                  besides those it holds are written behind them; nothing
+ *                  else is written
+ *   cache_seqlens: device [B]: L_b, read only
+ *   cu_seqlens_q : device [B + 1]: 0 = cu[0] <= cu[1] <= ... <= cu[B] = total_q
+ *   free_pages   : device [num_free] page ids, taken from the front in row
+ *                  order (row 0's pages first)
+ *   slots        : device [total_q], written: the flat cache slot
+ *                  page * page_size + offset of every new token (for
+ *                  mxa_cache_write)
+ *   new_seqlens  : device [B], written: L_b + n_b (another buffer than
+ *                  cache_seqlens, which every CTA reads)
+ *   pages_used   : device [1], written: how many of free_pages were taken
+ * A row that needs more pages than its table is wide, or than the free list
+ * still holds when its turn comes, takes none: its tokens' slots are -1 and
+ * new_seqlens[b] = L_b tells the caller (so does every later row that needs a
+ * page once the list has run out; rows that need none go on).  Lengths
+ * outside [0, max_pages_per_seq * page_size], offsets that break their rule
+ * (both clamped; the slots are then unspecified) and page ids outside
+ * [0, num_pages) (slot -1) are reported by mxa_device_error as
+ * MXA_ERR_INVALID_ARG.
+ * Errors: MXA_ERR_INVALID_ARG (negative sizes, missing pointers, B = 0 with
+ * total_q > 0), MXA_ERR_UNSUPPORTED past 32-bit sizes. */
+MXA_API mxa_status_t mxa_extend_tables(int32_t *block_table, const int32_t *cache_seqlens,
+                                       const int32_t *cu_seqlens_q, const int32_t *free_pages, int B, int total_q,
+                                       int num_free, int page_size, int num_pages, int max_pages_per_seq,
+                                       int32_t *slots, int32_t *new_seqlens, int32_t *pages_used, void *stream);
+
+/* Write new keys and values into their cache slots:
+ * cache[slots[t] / page_size][slots[t] % page_size] = new[t] for K and V, bit
+ * for bit.
+ *   k_new, v_new : device [total, Hkv, D] dtype, tokens k_token_stride and
+ *                  v_token_stride elements apart (>= Hkv * D and a multiple of
+ *                  8: slices of one fused projection may be passed as they are)
+ *   slots        : device [total], from mxa_extend_tables; a token with slot
+ *                  -1 is left out, one outside [-1, num_pages * page_size) too,
+ *                  and mxa_device_error then reports MXA_ERR_INVALID_ARG.  Slots
+ *                  are distinct: a slot named twice holds 16-byte pieces of
+ *                  either token.
+ *   k_cache, v_cache : device [num_pages, page_size, Hkv, D] dtype
+ * Errors: MXA_ERR_INVALID_ARG, MXA_ERR_UNSUPPORTED for Hkv * D or a stride
+ * that is not a multiple of 8 elements, or a pool past 32-bit slots. */
+MXA_API mxa_status_t mxa_cache_write(const void *k_new, const void *v_new, long long k_token_stride,
+                                     long long v_token_stride, const int32_t *slots, int total, int Hkv, int D,
+                                     int num_pages, int page_size, mxa_dtype_t dtype, void *k_cache,
+                                     void *v_cache, void *stream);
+
 /* Decode rows that each have their own number of queries: the packed
  * (varlen) layout of flash_attn_varlen_func ("MXFlashAttn 1.4.0", its API
  * list), with the cu_seqlens_q offsets defined in

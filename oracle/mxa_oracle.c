@@ -103,14 +103,18 @@ static size_t kv_index(const int32_t *block_table, int max_pages_per_seq,
  *   cache_seqlens [B] int32, the number of valid keys L_b of each row
  *   out        [B, q_len, Hq, D] double
  *   lse        [B, Hq, q_len]    double (natural log)
+ *   window     0: none; else (causal only) the query at position p sees only
+ *              the keys j with j > p - window or j < sinks
  * Returns 0, or -1 on a bad shape argument.
  */
-int oracle_decode(const uint16_t *q, const uint16_t *k_cache,
-                  const uint16_t *v_cache, const int32_t *block_table,
-                  const int32_t *cache_seqlens, int B, int q_len, int Hq,
-                  int Hkv, int D, int page_size, int max_pages_per_seq,
-                  int dtype, double scale, int causal, double *out,
-                  double *lse) {
+int oracle_decode_window(const uint16_t *q, const uint16_t *k_cache,
+                         const uint16_t *v_cache, const int32_t *block_table,
+                         const int32_t *cache_seqlens, int B, int q_len,
+                         int Hq, int Hkv, int D, int page_size,
+                         int max_pages_per_seq, int dtype, double scale,
+                         int causal, int window, int sinks, double *out,
+                         double *lse) {
+  if (window < 0 || sinks < 0 || (window > 0 && !causal)) return -1;
   if (B < 0 || q_len < 1 || Hq < 1 || Hkv < 1 || D < 1 || page_size < 1 ||
       Hq % Hkv != 0)
     return -1;
@@ -138,6 +142,9 @@ int oracle_decode(const uint16_t *q, const uint16_t *k_cache,
       continue;
     }
 
+    /* keys in [sinks, low) are outside the window of position n - 1 */
+    const long low = window > 0 ? (long)n - window : 0;
+
     const uint16_t *qrow = q + (((size_t)b * q_len + t) * Hq + h) * (size_t)D;
     double *qd = (double *)malloc(sizeof(double) * (size_t)D);
     double *s = (double *)malloc(sizeof(double) * (size_t)n);
@@ -145,6 +152,10 @@ int oracle_decode(const uint16_t *q, const uint16_t *k_cache,
 
     /* scores s_j = scale * sum_d q[d] k_j[d] */
     for (int j = 0; j < n; ++j) {
+      if (j < low && j >= sinks) {
+        s[j] = -INFINITY; /* weight 0 */
+        continue;
+      }
       const uint16_t *krow =
           k_cache + kv_index(block_table, max_pages_per_seq, page_size, Hkv,
                              D, b, j, kvh);
@@ -166,6 +177,7 @@ int oracle_decode(const uint16_t *q, const uint16_t *k_cache,
     /* O = sum_j p_j v_j / l */
     for (int d = 0; d < D; ++d) o[d] = 0.0;
     for (int j = 0; j < n; ++j) {
+      if (j < low && j >= sinks) continue; /* a hidden value is not touched */
       const uint16_t *vrow =
           v_cache + kv_index(block_table, max_pages_per_seq, page_size, Hkv,
                              D, b, j, kvh);
@@ -178,6 +190,18 @@ int oracle_decode(const uint16_t *q, const uint16_t *k_cache,
     free(qd);
   }
   return 0;
+}
+
+int oracle_decode(const uint16_t *q, const uint16_t *k_cache,
+                  const uint16_t *v_cache, const int32_t *block_table,
+                  const int32_t *cache_seqlens, int B, int q_len, int Hq,
+                  int Hkv, int D, int page_size, int max_pages_per_seq,
+                  int dtype, double scale, int causal, double *out,
+                  double *lse) {
+  return oracle_decode_window(q, k_cache, v_cache, block_table, cache_seqlens,
+                              B, q_len, Hq, Hkv, D, page_size,
+                              max_pages_per_seq, dtype, scale, causal, 0, 0,
+                              out, lse);
 }
 
 /*

@@ -28,6 +28,9 @@ def _load():
         lib.oracle_decode.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I,
                                       ctypes.c_double, I, P, P]
         lib.oracle_decode.restype = I
+        lib.oracle_decode_window.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I,
+                                             ctypes.c_double, I, I, I, P, P]
+        lib.oracle_decode_window.restype = I
         lib.oracle_combine.argtypes = [P, P, I, ctypes.c_long, I, P, P]
         lib.oracle_combine.restype = I
         lib.oracle_f16_to_double.argtypes = [ctypes.c_uint16]
@@ -54,8 +57,12 @@ def _ptr(a: Optional[np.ndarray]):
 
 def decode(q, k_cache, v_cache, block_table, cache_seqlens, *, Hkv: int,
            page_size: int, dtype: str, scale: float, causal: bool,
-           max_pages_per_seq: Optional[int] = None) -> Tuple[np.ndarray, np.ndarray]:
+           max_pages_per_seq: Optional[int] = None, window: int = 0,
+           sinks: int = 0) -> Tuple[np.ndarray, np.ndarray]:
     """Exact attention in fp64.
+
+    With window > 0 (causal only) the query at position p sees only its last
+    `window` keys, j > p - window, and the first `sinks` keys.
 
     q [B, q_len, Hq, D]; k_cache/v_cache [num_pages, page_size, Hkv, D]
     (or [B, page_size, Hkv, D] when block_table is None); block_table
@@ -73,16 +80,18 @@ def decode(q, k_cache, v_cache, block_table, cache_seqlens, *, Hkv: int,
         mpps = bt.shape[1] if max_pages_per_seq is None else max_pages_per_seq
     out = np.empty((B, q_len, Hq, D), dtype=np.float64)
     lse = np.empty((B, Hq, q_len), dtype=np.float64)
-    rc = lib.oracle_decode(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(bt), _ptr(L), B, q_len, Hq,
-                           Hkv, D, page_size, mpps, BF16 if dtype == "bf16" else F16,
-                           float(scale), int(bool(causal)), _ptr(out), _ptr(lse))
+    rc = lib.oracle_decode_window(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(bt), _ptr(L), B, q_len, Hq,
+                                  Hkv, D, page_size, mpps, BF16 if dtype == "bf16" else F16,
+                                  float(scale), int(bool(causal)), int(window), int(sinks), _ptr(out),
+                                  _ptr(lse))
     if rc != 0:
         raise ValueError("oracle_decode: bad shape arguments")
     return out, lse
 
 
 def decode_varlen(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, Hkv: int,
-                  page_size: int, dtype: str, scale: float, causal: bool) -> Tuple[np.ndarray, np.ndarray]:
+                  page_size: int, dtype: str, scale: float, causal: bool, window: int = 0,
+                  sinks: int = 0) -> Tuple[np.ndarray, np.ndarray]:
     """Exact attention for rows with their own number of queries, in fp64.
 
     The packed-query layout of a varlen call: row b's queries are
@@ -115,7 +124,7 @@ def decode_varlen(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens,
         else:
             kc, vc = _bits(k_cache), _bits(v_cache)
         o, l = decode(qb[None, q0:q1], kc, vc, row_bt, L[b:b + 1], Hkv=Hkv, page_size=page_size,
-                      dtype=dtype, scale=scale, causal=causal)
+                      dtype=dtype, scale=scale, causal=causal, window=window, sinks=sinks)
         out[q0:q1] = o[0]
         lse[:, q0:q1] = l[0]
     return out, lse
@@ -150,6 +159,43 @@ def append_kv(k_cache, v_cache, k_new, v_new, block_table, cache_seqlens, *, pag
             kb[page, slot] = knb[b, t]
             vb[page, slot] = vnb[b, t]
     return kb, vb
+
+
+def extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, *, page_size: int, num_pages: int):
+    """Pages and slots of a step's new tokens, one request and one token at a time.
+
+    Returns (block_table, slots, new_seqlens, pages_used): the table with the
+    pages each request needs for its new tokens taken from the front of
+    free_pages in request order, every new token's flat slot page * page_size
+    + offset, the lengths after the step and the number of pages taken.  A
+    request whose pages do not fit its table, or which the free list cannot
+    serve (nor could it a request before it that needed pages), takes none.
+    """
+    bt = np.array(block_table, dtype=np.int64)
+    L = np.asarray(cache_seqlens, dtype=np.int64)
+    cu = np.asarray(cu_seqlens_q, dtype=np.int64)
+    free = np.asarray(free_pages, dtype=np.int64)
+    slots = np.full(int(cu[-1]), -1, dtype=np.int64)
+    new = L.copy()
+    used, ran_out = 0, False
+    for b in range(L.size):
+        n = int(cu[b + 1] - cu[b])
+        have = -(-int(L[b]) // page_size)
+        need = -(-int(L[b] + n) // page_size)
+        if need > bt.shape[1]:
+            continue
+        if need > have and (ran_out or used + need - have > free.size):
+            ran_out = True
+            continue
+        for p in range(have, need):
+            bt[b, p] = free[used]
+            used += 1
+        for t in range(n):
+            page = int(bt[b, (int(L[b]) + t) // page_size])
+            if 0 <= page < num_pages:
+                slots[cu[b] + t] = page * page_size + (int(L[b]) + t) % page_size
+        new[b] += n
+    return bt, slots, new, used
 
 
 def combine(o_part: np.ndarray, lse_part: np.ndarray) -> Tuple[np.ndarray, np.ndarray]:
