@@ -15,14 +15,17 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmxa.so")
-SOURCES = [os.path.join(CSRC, "mxa_kernels.cu"), os.path.join(CSRC, "mxa_api.cpp"),
-           os.path.join(CSRC, "mxa_noalloc.cu"), os.path.join(CSRC, "mxa_cache_ops.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("mxa_config.h", "mxa_device.cuh", "mxa_launch.h")] + \
+# (source, object, its own flags): the split kernel's instances of each head
+# dim are compiled apart, side by side
+UNITS = [("mxa_kernels.cu", "mxa_kernels_d%d.o" % d, ["-DMXA_HEAD_DIM=%d" % d]) for d in (64, 128, 256)] + \
+    [(f, f + ".o", []) for f in ("mxa_api.cpp", "mxa_noalloc.cu", "mxa_cache_ops.cu")]
+DEPS = sorted({os.path.join(CSRC, u[0]) for u in UNITS}) + \
+    [os.path.join(CSRC, f) for f in ("mxa_config.h", "mxa_device.cuh", "mxa_launch.h")] + \
     [os.path.join(INCLUDE, "mxa.h")]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-         "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr", "--split-compile=0",
+         "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",
          "-I" + INCLUDE, "-I" + CSRC]
 
 
@@ -37,9 +40,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     objs, running = [], []
-    for src in SOURCES:  # side by side: each takes seconds to minutes
-        obj = os.path.join(CSRC, os.path.basename(src) + ".o")
-        cmd = [NVCC, *FLAGS, "-c", src, "-o", obj]
+    for src, obj, extra in UNITS:
+        obj = os.path.join(CSRC, obj)
+        cmd = [NVCC, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose and src.endswith(".cu"):
             cmd += ["-Xptxas", "-v"]
         running.append((cmd, subprocess.Popen(cmd)))

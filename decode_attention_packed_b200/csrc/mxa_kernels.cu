@@ -32,6 +32,9 @@
 //    RightDownCausal mask for the draft tokens of a speculative step; 源码级
 //    原理: a balanced division of the KV work over the cores, with a reduce
 //    for rows whose keys span several cores.
+//
+// Compiled once per head dim (MXA_HEAD_DIM = 64, 128, 256), side by side: the
+// instances of one head dim take a minute or two.
 #include <type_traits>
 
 #include "mxa_config.h"
@@ -40,7 +43,7 @@
 
 namespace mxa {
 
-__device__ int g_mxa_err = 0;
+static __device__ int g_mxa_err = 0;  // this head dim's failure record
 
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -1587,6 +1590,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
   }
 }
 
+#if MXA_HEAD_DIM == 128  // the parts that no head dim instantiates
 // ---------------------------------------------------------------------------
 // mxa_combine: split results in the uniform layout o_part[S, B, q_len, Hq, D],
 // lse_part[S, B, Hq, q_len].  One warp per (b, t, h) row.
@@ -1632,6 +1636,7 @@ __global__ void __launch_bounds__(128)
         make_uint2(pack2<kBf16>(acc.x, acc.y), pack2<kBf16>(acc.z, acc.w));
   }
 }
+#endif
 
 }  // namespace mxa
 
@@ -1824,28 +1829,14 @@ mxa_status_t launch_typed(const DecodeLaunch &L, cudaStream_t stream) {
 
 }  // namespace
 
-mxa_status_t launch_decode(const DecodeLaunch &L, cudaStream_t stream) {
-  const bool bf16 = L.p.dtype == MXA_BF16;
-  if (L.p.D == 128) return bf16 ? launch_typed<128, true>(L, stream) : launch_typed<128, false>(L, stream);
-  if (L.p.D == 64) return bf16 ? launch_typed<64, true>(L, stream) : launch_typed<64, false>(L, stream);
-  if (L.p.D == 256) return bf16 ? launch_typed<256, true>(L, stream) : launch_typed<256, false>(L, stream);
-  return MXA_ERR_UNSUPPORTED;
+template <>
+mxa_status_t launch_split<MXA_HEAD_DIM>(const DecodeLaunch &L, cudaStream_t stream) {
+  return L.p.dtype == MXA_BF16 ? launch_typed<MXA_HEAD_DIM, true>(L, stream)
+                               : launch_typed<MXA_HEAD_DIM, false>(L, stream);
 }
 
-mxa_status_t launch_combine(const float *o_part, const float *lse_part, int num_splits, int B,
-                            int q_len, int Hq, int D, mxa_dtype_t dtype, void *out, float *lse,
-                            cudaStream_t stream) {
-  const long long rows = (long long)B * q_len * Hq;
-  if (rows == 0) return MXA_OK;
-  const unsigned blocks = (unsigned)((rows + 3) / 4);
-  if (dtype == MXA_BF16)
-    mxa_combine_kernel<true><<<blocks, 128, 0, stream>>>(o_part, lse_part, num_splits, B, q_len, Hq, D, out, lse);
-  else
-    mxa_combine_kernel<false><<<blocks, 128, 0, stream>>>(o_part, lse_part, num_splits, B, q_len, Hq, D, out, lse);
-  return cudaGetLastError() == cudaSuccess ? MXA_OK : MXA_ERR_CUDA;
-}
-
-mxa_status_t device_error_word(int **word) {
+template <>
+mxa_status_t split_error_word<MXA_HEAD_DIM>(int **word) {
   static std::mutex mu;
   static int *cache[kMaxDevices] = {};
   int device = 0;
@@ -1863,15 +1854,42 @@ mxa_status_t device_error_word(int **word) {
   return MXA_OK;
 }
 
+#if MXA_HEAD_DIM == 128
+mxa_status_t launch_decode(const DecodeLaunch &L, cudaStream_t stream) {
+  if (L.p.D == 128) return launch_split<128>(L, stream);
+  if (L.p.D == 64) return launch_split<64>(L, stream);
+  if (L.p.D == 256) return launch_split<256>(L, stream);
+  return MXA_ERR_UNSUPPORTED;
+}
+
+mxa_status_t launch_combine(const float *o_part, const float *lse_part, int num_splits, int B,
+                            int q_len, int Hq, int D, mxa_dtype_t dtype, void *out, float *lse,
+                            cudaStream_t stream) {
+  const long long rows = (long long)B * q_len * Hq;
+  if (rows == 0) return MXA_OK;
+  const unsigned blocks = (unsigned)((rows + 3) / 4);
+  if (dtype == MXA_BF16)
+    mxa_combine_kernel<true><<<blocks, 128, 0, stream>>>(o_part, lse_part, num_splits, B, q_len, Hq, D, out, lse);
+  else
+    mxa_combine_kernel<false><<<blocks, 128, 0, stream>>>(o_part, lse_part, num_splits, B, q_len, Hq, D, out, lse);
+  return cudaGetLastError() == cudaSuccess ? MXA_OK : MXA_ERR_CUDA;
+}
+
+mxa_status_t device_error_word(int **word) { return split_error_word<128>(word); }
+
 mxa_status_t read_device_error(int reset, int *flags) {
-  int v = 0;
   if (cudaDeviceSynchronize() != cudaSuccess) return MXA_ERR_CUDA;
-  if (cudaMemcpyFromSymbol(&v, g_mxa_err, sizeof(int)) != cudaSuccess) return MXA_ERR_CUDA;
-  if (reset) {
+  *flags = 0;
+  mxa_status_t (*const words[])(int **) = {split_error_word<64>, split_error_word<128>, split_error_word<256>};
+  for (auto word : words) {
+    int *p = nullptr, v = 0;
     const int zero = 0;
-    if (cudaMemcpyToSymbol(g_mxa_err, &zero, sizeof(int)) != cudaSuccess) return MXA_ERR_CUDA;
+    if (word(&p) != MXA_OK || cudaMemcpy(&v, p, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
+      return MXA_ERR_CUDA;
+    if (reset && v != 0 && cudaMemcpy(p, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
+      return MXA_ERR_CUDA;
+    *flags |= v;
   }
-  *flags = v;
   return MXA_OK;
 }
 
@@ -1892,5 +1910,6 @@ mxa_status_t current_sm_count(int *sm_count) {
   *sm_count = n;
   return MXA_OK;
 }
+#endif
 
 }  // namespace mxa

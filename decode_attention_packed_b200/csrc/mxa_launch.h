@@ -79,6 +79,19 @@ inline long long window_keys(const mxa_decode_params_t &p, int window, int sinks
   return keys < p.max_seqlen_k ? keys : p.max_seqlen_k;
 }
 
+// The split kernel's instances of one head dim (64, 128 or 256), each in its
+// own translation unit with its own failure record.
+template <int D>
+mxa_status_t launch_split(const DecodeLaunch &L, cudaStream_t stream);
+template <int D>
+mxa_status_t split_error_word(int **word);
+template <> mxa_status_t launch_split<64>(const DecodeLaunch &L, cudaStream_t stream);
+template <> mxa_status_t launch_split<128>(const DecodeLaunch &L, cudaStream_t stream);
+template <> mxa_status_t launch_split<256>(const DecodeLaunch &L, cudaStream_t stream);
+template <> mxa_status_t split_error_word<64>(int **word);
+template <> mxa_status_t split_error_word<128>(int **word);
+template <> mxa_status_t split_error_word<256>(int **word);
+
 // Launch the split kernel (split units are merged inside it).
 mxa_status_t launch_decode(const DecodeLaunch &L, cudaStream_t stream);
 
@@ -112,8 +125,8 @@ mxa_status_t launch_combine(const float *o_part, const float *lse_part, int num_
                             int q_len, int Hq, int D, mxa_dtype_t dtype, void *out, float *lse,
                             cudaStream_t stream);
 
-// Address of the current device's failure record, for kernels outside the
-// translation unit that defines it (looked up once per device).
+// Address of a failure record on the current device, for the other kernels
+// (looked up once per device).
 mxa_status_t device_error_word(int **word);
 
 // Read (and optionally clear) the device-side failure record of the current device.
