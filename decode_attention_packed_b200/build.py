@@ -18,9 +18,10 @@ LIB = os.path.join(HERE, "libmxa.so")
 # (source, object, its own flags): the split kernel's instances of each head
 # dim are compiled apart, side by side
 UNITS = [("mxa_kernels.cu", "mxa_kernels_d%d.o" % d, ["-DMXA_HEAD_DIM=%d" % d]) for d in (64, 128, 256)] + \
-    [(f, f + ".o", []) for f in ("mxa_api.cpp", "mxa_noalloc.cu", "mxa_cache_ops.cu")]
+    [(f, f + ".o", []) for f in ("mxa_api.cpp", "mxa_noalloc.cu", "mxa_cache_ops.cu", "mxa_prefill.cu")]
 DEPS = sorted({os.path.join(CSRC, u[0]) for u in UNITS}) + \
-    [os.path.join(CSRC, f) for f in ("mxa_config.h", "mxa_device.cuh", "mxa_launch.h")] + \
+    [os.path.join(CSRC, f) for f in ("mxa_config.h", "mxa_device.cuh", "mxa_launch.h", "mxa_prefill.h",
+                                    "mxa_tcgen05.cuh", "mxa_tmap.h")] + \
     [os.path.join(INCLUDE, "mxa.h")]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

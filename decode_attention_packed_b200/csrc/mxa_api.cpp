@@ -7,6 +7,7 @@
 #include "mxa.h"
 #include "mxa_config.h"
 #include "mxa_launch.h"
+#include "mxa_prefill.h"
 
 namespace {
 
@@ -115,6 +116,22 @@ mxa_status_t prepare_decode(const void *q, const void *k_cache, const void *v_ca
   L.total_q = 0;
   L.out_f32 = 0;
   L.window = L.sinks = 0;
+  return MXA_OK;
+}
+
+// Shape checks of the chunk attention (block_table unknown: the page size is
+// checked by the run).
+mxa_status_t check_prefill(const mxa_decode_params_t *p, int total_q) {
+  if (p == nullptr || total_q < 0) return MXA_ERR_INVALID_ARG;
+  if (p->B < 0 || p->q_len < 1 || p->Hq < 1 || p->Hkv < 1 || p->Hq % p->Hkv != 0) return MXA_ERR_INVALID_ARG;
+  if (p->dtype != MXA_F16 && p->dtype != MXA_BF16) return MXA_ERR_INVALID_ARG;
+  if (p->page_size < 1 || p->num_pages < 1 || p->max_seqlen_k < 0 || p->max_pages_per_seq < 1)
+    return MXA_ERR_INVALID_ARG;
+  if (p->B == 0 && total_q > 0) return MXA_ERR_INVALID_ARG;
+  if (p->D != 64 && p->D != 128 && p->D != 256) return MXA_ERR_UNSUPPORTED;
+  if (p->Hq / p->Hkv > 128 || p->B > kMaxBalancedRows) return MXA_ERR_UNSUPPORTED;
+  if ((long long)p->num_pages * p->page_size > INT32_MAX) return MXA_ERR_UNSUPPORTED;  // TMA coordinates
+  if ((long long)total_q + p->max_seqlen_k > INT32_MAX) return MXA_ERR_UNSUPPORTED;    // positions
   return MXA_OK;
 }
 
@@ -354,6 +371,59 @@ mxa_status_t mxa_decode_fwd_window(const void *q, void *k_cache, void *v_cache, 
     L.v_new = v_new;
   }
   return launch_decode(L, static_cast<cudaStream_t>(stream));
+}
+
+size_t mxa_prefill_workspace_size(const mxa_decode_params_t *p, int total_q) {
+  int sm_count = 0;
+  if (check_prefill(p, total_q) != MXA_OK || current_sm_count(&sm_count) != MXA_OK) return SIZE_MAX;
+  return plan_prefill(*p, total_q, sm_count).workspace_bytes;
+}
+
+mxa_status_t mxa_prefill_fwd(const void *q, const int32_t *cu_seqlens_q, int total_q, const void *k_cache,
+                             const void *v_cache, const int32_t *block_table, const int32_t *cache_seqlens,
+                             const mxa_decode_params_t *p, float scale, int causal, int window, int sinks,
+                             void *workspace, size_t workspace_bytes, void *out, float *lse, void *stream) {
+  mxa_status_t st = check_prefill(p, total_q);
+  if (st != MXA_OK) return st;
+  if (block_table == nullptr) {
+    if (p->num_pages != p->B && p->B > 0) return MXA_ERR_INVALID_ARG;
+    if (p->page_size < p->max_seqlen_k) return MXA_ERR_INVALID_ARG;
+  } else {
+    if ((long long)p->max_pages_per_seq * p->page_size < p->max_seqlen_k) return MXA_ERR_INVALID_ARG;
+    if (p->page_size % 8 != 0) return MXA_ERR_UNSUPPORTED;
+  }
+  if (!isfinite(scale) || (causal != 0 && causal != 1) || window < 0 || sinks < 0) return MXA_ERR_INVALID_ARG;
+  if ((window > 0 && causal != 1) || (window == 0 && sinks > 0)) return MXA_ERR_INVALID_ARG;
+  if (total_q == 0) return MXA_OK;  // no query: nothing is written
+  if (q == nullptr || cu_seqlens_q == nullptr || k_cache == nullptr || v_cache == nullptr ||
+      cache_seqlens == nullptr || out == nullptr)
+    return MXA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(cu_seqlens_q, 4) || !aligned(cache_seqlens, 4) || !aligned(block_table, 4) || !aligned(lse, 4))
+    return MXA_ERR_INVALID_ARG;
+  int sm_count = 0;
+  st = current_sm_count(&sm_count);
+  if (st != MXA_OK) return st;
+  PrefillLaunch L = {};
+  L.plan = plan_prefill(*p, total_q, sm_count);
+  if (workspace == nullptr || workspace_bytes < L.plan.workspace_bytes || !aligned(workspace, 256))
+    return MXA_ERR_WORKSPACE;
+  L.q = q;
+  L.k_cache = k_cache;
+  L.v_cache = v_cache;
+  L.cu_q = cu_seqlens_q;
+  L.block_table = block_table;
+  L.seqlens = cache_seqlens;
+  L.total_q = total_q;
+  L.out = out;
+  L.lse = lse;
+  L.workspace = workspace;
+  L.p = *p;
+  L.scale = scale;
+  L.causal = causal;
+  L.window = window;
+  L.sinks = sinks;
+  return launch_prefill(L, static_cast<cudaStream_t>(stream));
 }
 
 mxa_status_t mxa_extend_tables(int32_t *block_table, const int32_t *cache_seqlens, const int32_t *cu_seqlens_q,

@@ -1643,83 +1643,15 @@ __global__ void __launch_bounds__(128)
 // ===========================================================================
 // Host side: tensor maps and launches
 // ===========================================================================
-#include <cudaTypedefs.h>
-
 #include <atomic>
 #include <mutex>
+
+#include "mxa_tmap.h"
 
 namespace mxa {
 namespace {
 
 constexpr int kMaxDevices = 64;
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static std::once_flag once;
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  std::call_once(once, [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
-// 3-D map {D, Hkv, pool tokens} of a K or V pool; box {64 elements, 1 head,
-// box_tokens tokens}, 128-byte swizzle, zero fill out of bounds.  L2 fills
-// are promoted to whole rows of one head: 256 bytes for D >= 128 (the
-// second 64-column box of a row then hits), 128 bytes for D = 64, whose
-// 128-byte row a 256-byte fill would widen into the next head's row, read
-// from DRAM a second time by the CTA of that head once L2 has let it go.
-bool encode_kv_map(CUtensorMap *m, const void *base, int D, int Hkv, long long pool_tokens,
-                   int box_tokens, bool bf16) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (enc == nullptr) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)pool_tokens};
-  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2};
-  cuuint32_t box[3] = {64u, 1u, (cuuint32_t)box_tokens};
-  cuuint32_t estride[3] = {1u, 1u, 1u};
-  CUresult r = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-                   const_cast<void *>(base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B,
-                   D >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-// The K and V maps of a call, from a small per-thread cache: a decode loop
-// calls with the same cache buffers step after step, and encoding the two
-// maps is a noticeable part of the host time of a short call.  The key is
-// every input of the encoding, so a hit is always the map the call needs.
-bool kv_maps(TmapPair *tm, const void *k, const void *v, int D, int Hkv, long long pool_tokens, int box_tokens,
-             bool bf16) {
-  struct Entry {
-    const void *k, *v;
-    long long pool_tokens;
-    int D, Hkv, box_tokens;
-    bool bf16, used;
-    TmapPair tm;
-  };
-  constexpr int kEntries = 4;
-  thread_local Entry cache[kEntries] = {};
-  thread_local int next = 0;
-  for (int i = 0; i < kEntries; ++i) {
-    const Entry &e = cache[i];
-    if (e.used && e.k == k && e.v == v && e.pool_tokens == pool_tokens && e.D == D && e.Hkv == Hkv &&
-        e.box_tokens == box_tokens && e.bf16 == bf16) {
-      *tm = e.tm;
-      return true;
-    }
-  }
-  if (!encode_kv_map(&tm->k, k, D, Hkv, pool_tokens, box_tokens, bf16) ||
-      !encode_kv_map(&tm->v, v, D, Hkv, pool_tokens, box_tokens, bf16))
-    return false;
-  Entry &e = cache[next];
-  next = (next + 1) % kEntries;
-  e = Entry{k, v, pool_tokens, D, Hkv, box_tokens, bf16, true, *tm};
-  return true;
-}
 
 template <int D, bool kBf16, bool kAppend, bool kVarlen, bool kWindow>
 cudaError_t prepare_split_kernel(int device) {
@@ -1776,7 +1708,7 @@ mxa_status_t launch_typed(const DecodeLaunch &L, cudaStream_t stream) {
   a.causal = L.causal;
   a.schedule = plan.schedule;
   a.splits = plan.num_splits;
-  a.window = L.window;
+  a.window = L.window < p.max_seqlen_k ? L.window : p.max_seqlen_k;  // a longer one hides nothing
   a.sinks = L.sinks;
   const int max_blocks = (int)(((window ? window_keys(p, L.window, L.sinks) : p.max_seqlen_k) + T - 1) / T);
   a.chunk_blocks = plan.schedule == MXA_SCHED_UNIFORM ? (max_blocks + plan.num_splits - 1) / plan.num_splits : 1;

@@ -1,0 +1,906 @@
+// Attention of chunks of new tokens over a paged grouped-query cache, for
+// sm_100a (mxa_prefill_fwd).
+//
+//   O = softmax(scale Q K^T + mask) V,   LSE = ln sum_j exp(scale q . k_j)
+//
+// Each CTA walks a contiguous share of the work with three roles:
+//  - a producer warp finds the CTA's share, gathers K and V pages through the
+//    block table with TMA into a ring of shared-memory slots, and loads the
+//    packed query rows;
+//  - an issuing warp runs S = Q K^T and O += P V on the tensor cores
+//    (tcgen05, accumulators and P in tensor memory);
+//  - one or two softmax warpgroups, one thread per packed query row, turn S
+//    into P with a running maximum and sum, and write the rows out.
+//
+// Units.  The G query heads of one KV head are packed into the rows of a
+// tile, row m = t * G + g, so a KV byte serves all of them: a 128-row tile
+// holds floor(128 / G) tokens.  A unit is (batch row, KV head, group of
+// tiles): two tiles for head dims 64 and 128 (while one tile's scores are in
+// the softmax, the tensor cores work on the other's), one for 256, whose
+// accumulator fills half of tensor memory (two score buffers take the
+// second tile's place).
+//
+// Split.  All units, each a fixed cost plus its visible KV blocks, are laid
+// end to end and cut into equal contiguous ranges, one per CTA: ragged
+// batches, causal triangles and single long rows all give every CTA the same
+// work.  A unit cut by a range's end leaves float32 pieces with their LSEs in
+// the workspace, which a second small kernel merges.
+#include <type_traits>
+
+#include "mxa_config.h"
+#include "mxa_device.cuh"
+#include "mxa_launch.h"
+#include "mxa_prefill.h"
+#include "mxa_tcgen05.cuh"
+#include "mxa_tmap.h"
+
+namespace mxa {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kTileRows = 128;
+constexpr int kDescs = 4;  // segments published ahead
+
+template <int D>
+struct Cfg {
+  static constexpr int NT = D <= 128 ? 2 : 1;       // tiles of a unit
+  static constexpr int T = D <= 128 ? 128 : 64;     // keys of a block
+  static constexpr int CH = D / 64;                 // 64-column chunks of a row
+  static constexpr int kSoftmaxWarps = 4 * NT;
+  static constexpr int kMmaWarp = kSoftmaxWarps, kProducerWarp = kSoftmaxWarps + 1;
+  static constexpr int kThreads = 128 * (NT + 1);
+  static constexpr int kSlotBytes = T * D * 2;      // one block of K or of V
+  static constexpr int kSlots = 160 * 1024 / kSlotBytes;
+  static constexpr int kQBytes = kTileRows * D * 2;
+  // tensor memory: two score buffers of T columns (P over the first half of
+  // each), then the tiles' accumulators
+  static constexpr int kOCol = 256;
+  // shared memory
+  static constexpr int kQOff = kSlots * kSlotBytes;
+  static constexpr int kDescOff = kQOff + NT * kQBytes;
+  static constexpr int kBarOff = kDescOff + kDescs * 64;
+  static constexpr int kSmem = kBarOff + 512;
+  // barriers
+  static constexpr int B_FULL = 0, B_EMPTY = kSlots, B_SFULL = 2 * kSlots, B_PREADY = B_SFULL + 2;
+  static constexpr int B_OFULL = B_PREADY + 2, B_QFULL = B_OFULL + 2, B_QEMPTY = B_QFULL + 1;
+  static constexpr int B_DFULL = B_QEMPTY + 1, B_DEMPTY = B_DFULL + kDescs, B_COUNT = B_DEMPTY + kDescs;
+  static_assert(B_COUNT * 8 + 16 <= 512 && kSmem <= 227 * 1024, "shared memory");
+};
+
+// A contiguous range of one unit's KV blocks, as the producer publishes it.
+struct Segment {
+  int b, h, it;      // batch row, KV head, group of tiles
+  int q0, qn, L;     // the row's first packed token, its tokens and its keys
+  int beg, end;      // blocks [beg, end) of the unit's own numbering
+  int kind;          // 0: the whole unit; 1 / 2: piece in the CTA's head / tail slot; -1: no more work
+  int c_first, n_pieces;
+  int pad[5];
+};
+static_assert(sizeof(Segment) == 64, "descriptor slot");
+
+// What the masks leave of a group of tiles: keys [0, sinks) and [low, hi),
+// in blocks numbered without the gap between them.  Never less than one
+// block, so that a group that sees no key still has a place in the work.
+struct Span {
+  int hi, low, ns, skip, nb;
+  __device__ __forceinline__ int block(int v) const { return v < ns ? v : v + skip; }
+};
+template <int T>
+__device__ __forceinline__ Span span_of(const PrefillArgs &a, int L, int qn, int t0, int t1) {
+  Span s;
+  const int p0 = L - qn + t0;  // position of the first token
+  s.hi = a.causal ? max(0, min(L, L - qn + t1)) : L;
+  const long long low = a.window > 0 ? (long long)p0 + 1 - a.window : 0;
+  s.low = low > 0 ? (int)low : 0;
+  const int first = s.low / T;
+  s.ns = min((min(a.sinks, s.hi) + T - 1) / T, first);
+  s.skip = first - s.ns;
+  s.nb = max(1, (s.hi + T - 1) / T - s.skip);
+  return s;
+}
+
+__device__ __forceinline__ void row_of(const PrefillArgs &a, int b, int &q0, int &qn, int &L) {
+  const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1], l = a.seqlens[b];
+  const int s = min(max(c0, 0), a.total_q), e = min(max(c1, s), a.total_q);
+  q0 = s;
+  qn = min(e - s, a.max_q);
+  L = min(max(l, 0), a.max_seqlen_k);
+}
+
+// Breaches of the call's contract by row b's inputs (clamped by row_of).
+__device__ __forceinline__ void check_row(const PrefillArgs &a, int b) {
+  const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1], l = a.seqlens[b];
+  int bad = 0;
+  if (l < 0 || l > a.max_seqlen_k) bad |= kErrBadLen;
+  if (c1 < c0 || (long long)c1 - c0 > a.max_q || (b == 0 && c0 != 0) || (b == a.B - 1 && c1 != a.total_q))
+    bad |= kErrBadOffsets;
+  if (bad) atomicOr(a.err, bad);
+}
+
+// Place in the work: block `blk` of unit (b, h, it) is position x.
+struct Walk {
+  int b, h, it, tiles;
+  int q0, qn, L;
+  int blk, nb;
+  long long x, end, per_cta;
+};
+
+template <int D>
+__device__ __forceinline__ Span walk_span(const PrefillArgs &a, const Walk &w) {
+  constexpr int NT = Cfg<D>::NT;
+  const int t0 = w.it * NT * a.TQ;
+  return span_of<Cfg<D>::T>(a, w.L, w.qn, t0, min(t0 + NT * a.TQ, w.qn));
+}
+
+// The segment at the walk, which moves past it and past the fixed cost of
+// the unit that follows.
+template <int D>
+__device__ Segment walk_take(const PrefillArgs &a, Walk &w) {
+  Segment s;
+  const long long room = w.end - w.x;
+  const int len = (int)min((long long)(w.nb - w.blk), room);
+  s.b = w.b; s.h = w.h; s.it = w.it;
+  s.q0 = w.q0; s.qn = w.qn; s.L = w.L;
+  s.beg = w.blk;
+  s.end = w.blk + len;
+  s.kind = (s.beg == 0 && s.end == w.nb) ? 0 : s.beg > 0 ? 1 : 2;
+  const long long xs = w.x - w.blk;
+  s.c_first = (int)(xs / w.per_cta);
+  s.n_pieces = (int)((xs + w.nb - 1) / w.per_cta) - s.c_first + 1;
+  w.x += len;
+  w.blk += len;
+  if (w.blk == w.nb && w.x < w.end) {
+    w.blk = 0;
+    if (++w.it == w.tiles) {
+      w.it = 0;
+      if (++w.h == a.Hkv) {
+        w.h = 0;
+        do {
+          if (++w.b == a.B) {
+            w.x = w.end;
+            return s;
+          }
+          row_of(a, w.b, w.q0, w.qn, w.L);
+        } while (w.qn == 0);
+        w.tiles = (w.qn + Cfg<D>::NT * a.TQ - 1) / (Cfg<D>::NT * a.TQ);
+      }
+    }
+    w.nb = walk_span<D>(a, w).nb;
+    w.x += a.unit_cost;
+  }
+  return s;
+}
+
+// Positions of one KV head's units of a row, over the lanes of a warp.
+template <int D>
+__device__ __forceinline__ long long row_positions(const PrefillArgs &a, int qn, int L, int lane) {
+  constexpr int NT = Cfg<D>::NT;
+  const int tiles = (qn + NT * a.TQ - 1) / (NT * a.TQ);
+  long long sum = 0;
+  for (int it = lane; it < tiles; it += 32) {
+    const int t0 = it * NT * a.TQ;
+    sum += a.unit_cost + span_of<Cfg<D>::T>(a, L, qn, t0, min(t0 + NT * a.TQ, qn)).nb;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// This CTA's range, from the rows' positions (`rows`, of one KV head each, in
+// shared memory); one warp.
+template <int D>
+__device__ Walk walk_start(const PrefillArgs &a, long long *rows, int lane) {
+  constexpr int NT = Cfg<D>::NT;
+  Walk w;
+  w.b = w.h = w.it = w.tiles = w.q0 = w.qn = w.L = w.blk = w.nb = 0;
+  w.x = w.end = 0;
+  w.per_cta = 1;
+  const int chunk = (a.B + 31) / 32;
+  const int lo = min(lane * chunk, a.B), hi = min(lo + chunk, a.B);
+  long long sum = 0;
+  for (int i = lo; i < hi; ++i) sum += rows[i];
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const long long total = __shfl_sync(0xffffffffu, incl, 31) * a.Hkv;
+  long long run = incl - sum;
+  for (int i = lo; i < hi; ++i) {
+    run += rows[i];
+    rows[i] = run;
+  }
+  __syncwarp();
+  if (total == 0) return w;
+  w.per_cta = (total + gridDim.x - 1) / gridDim.x;
+  const long long x0 = (long long)blockIdx.x * w.per_cta;
+  if (x0 >= total) return w;
+  w.end = min(x0 + w.per_cta, total);
+  int b0 = 0, b1 = a.B - 1;  // first row whose positions end past x0
+  while (b0 < b1) {
+    const int mid = (b0 + b1) >> 1;
+    if (rows[mid] * a.Hkv > x0) b1 = mid; else b0 = mid + 1;
+  }
+  w.b = b0;
+  row_of(a, w.b, w.q0, w.qn, w.L);
+  w.tiles = (w.qn + NT * a.TQ - 1) / (NT * a.TQ);
+  const long long pre = w.b > 0 ? rows[w.b - 1] : 0, width = rows[w.b] - pre;
+  const long long off = x0 - pre * a.Hkv;
+  w.h = (int)(off / width);
+  const long long in_head = off - w.h * width;
+  // the group of tiles that holds position in_head: scan them 32 at a time
+  long long before = 0;
+  for (int i0 = 0;; i0 += 32) {
+    const int it = i0 + lane, t0 = it * NT * a.TQ;
+    const int c = it < w.tiles ? a.unit_cost + span_of<Cfg<D>::T>(a, w.L, w.qn, t0, min(t0 + NT * a.TQ, w.qn)).nb : 0;
+    long long upto = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    upto += before;
+    const unsigned past = __ballot_sync(0xffffffffu, upto > in_head);
+    if (past != 0) {
+      const int l = __ffs(past) - 1;
+      w.it = i0 + l;
+      w.nb = __shfl_sync(0xffffffffu, c, l) - a.unit_cost;
+      const long long start = __shfl_sync(0xffffffffu, upto - c, l);
+      const int pos = (int)(in_head - start);
+      w.blk = pos > a.unit_cost ? pos - a.unit_cost : 0;
+      w.x = x0 - pos + a.unit_cost + w.blk;
+      break;
+    }
+    before = __shfl_sync(0xffffffffu, upto, 31);
+    if (i0 + 32 >= w.tiles) break;  // not reached: in_head < width
+  }
+  if (w.x > w.end) w.x = w.end;  // the range ends inside the unit's fixed cost
+  return w;
+}
+
+// ---------------------------------------------------------------------------
+// Producer warp
+// ---------------------------------------------------------------------------
+template <int D, bool kBf16>
+__device__ void producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *smem, int lane) {
+  using C = Cfg<D>;
+  constexpr int T = C::T, NT = C::NT;
+  const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
+  Segment *descs = reinterpret_cast<Segment *>(smem + C::kDescOff);
+  if (lane == 0) {
+    prefetch_tmap(&tm.kv.k);
+    prefetch_tmap(&tm.kv.v);
+    prefetch_tmap(&tm.q);
+  }
+  Walk w = walk_start<D>(a, reinterpret_cast<long long *>(smem), lane);
+  fence_proxy_async_smem();  // the scan's accesses precede the ring's loads
+  __syncwarp();
+  const int bt = a.box_tokens;
+  int slot_n = 0, seg_n = 0;
+  bool ok = true, bad_page = false;
+  // page of the box at token `tok` of row b, for this lane
+  auto page_at = [&](int b, int tok) {
+    const int p = tok / a.page_size;
+    return p < a.mpps ? a.block_table[(size_t)b * a.mpps + p] : -1;
+  };
+  for (;;) {
+    const bool more = w.x < w.end;
+    const Walk at = w;
+    Segment s;
+    if (more) s = walk_take<D>(a, w);
+    else s.kind = -1;
+    const int d = seg_n % kDescs;
+    if (!warp_wait_bounded(bars + 8 * (C::B_DEMPTY + d), ((seg_n / kDescs) & 1) ^ 1, a.err, kErrWaitQ, lane)) {
+      ok = false;
+      break;
+    }
+    if (lane == 0) {
+      descs[d] = s;
+      mbar_arrive(bars + 8 * (C::B_DFULL + d));
+    }
+    __syncwarp();
+    if (!more) break;
+    // queries: free once the unit before has issued its last scores
+    if (!warp_wait_bounded(bars + 8 * C::B_QEMPTY, (seg_n & 1) ^ 1, a.err, kErrWaitQ, lane)) {
+      ok = false;
+      break;
+    }
+    const int t0 = s.it * NT * a.TQ;
+    const int tiles = min(NT, (s.qn - t0 + a.TQ - 1) / a.TQ);
+    if (lane == 0) mbar_arrive_expect_tx(bars + 8 * C::B_QFULL, (uint32_t)(tiles * C::CH * a.TQ * a.G * 128));
+    __syncwarp();
+    if (lane < tiles * C::CH) {
+      const int t = lane / C::CH, ch = lane % C::CH;
+      tma_load_3d(sbase + C::kQOff + t * C::kQBytes + ch * (kTileRows * 128), &tm.q, ch * 64, s.h * a.G,
+                  s.q0 + t0 + t * a.TQ, bars + 8 * C::B_QFULL);
+    }
+    ++seg_n;
+    const Span span = walk_span<D>(a, at);
+    int page = 0;
+    if (!a.contiguous && lane < T / bt) page = page_at(s.b, span.block(s.beg) * T + lane * bt);
+    for (int blk = s.beg; blk < s.end && ok; ++blk) {
+      const int tok0 = span.block(blk) * T;
+      const int valid = max(0, min(T, span.hi - tok0));
+      const int nbox = (valid + bt - 1) / bt;
+      int next_page = 0;  // of the next block, on its way while this one is issued
+      if (!a.contiguous && blk + 1 < s.end && lane < T / bt) next_page = page_at(s.b, span.block(blk + 1) * T + lane * bt);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int sl = slot_n % C::kSlots;
+        const uint32_t full = bars + 8 * (C::B_FULL + sl);
+        if (!warp_wait_bounded(bars + 8 * (C::B_EMPTY + sl), ((slot_n / C::kSlots) & 1) ^ 1, a.err, kErrWaitEmpty, lane)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(nbox * bt * D * 2));
+        __syncwarp();
+        for (int op0 = 0; op0 < nbox * C::CH; op0 += 32) {
+          const int op = op0 + lane, box = op / C::CH, ch = op % C::CH;
+          const int tok = tok0 + box * bt;
+          int pg = __shfl_sync(0xffffffffu, page, box & 31);
+          int row = s.b * a.page_size + tok;
+          if (!a.contiguous) {
+            // A box of hidden keys only is never read, whatever its table entry
+            // holds; a page outside the pool reads as zeros and is reported.
+            // Both are placed at negative rows, which the map fills with zeros.
+            const bool hidden = tok >= a.sinks && tok + bt <= span.low;
+            if (hidden || pg < 0 || pg >= a.num_pages) {
+              bad_page |= !hidden && op < nbox * C::CH;
+              pg = -1;
+            }
+            row = pg < 0 ? -a.page_size + tok % a.page_size : pg * a.page_size + tok % a.page_size;
+          }
+          if (op < nbox * C::CH)
+            tma_load_3d(sbase + sl * C::kSlotBytes + ch * (T * 128) + box * bt * 128,
+                        kv ? (const void *)&tm.kv.v : (const void *)&tm.kv.k, ch * 64, s.h, row, full);
+        }
+        ++slot_n;
+      }
+      page = next_page;
+    }
+    if (!ok) break;
+  }
+  if (__any_sync(0xffffffffu, bad_page) && lane == 0) atomicOr(a.err, kErrBadPage);
+  // Leave only when the copies issued here have landed.
+  for (int j = max(0, slot_n - C::kSlots); j < slot_n; ++j)
+    mbar_wait_bounded(bars + 8 * (C::B_FULL + j % C::kSlots), (j / C::kSlots) & 1, a.err, kErrDrain);
+  if (seg_n > 0) mbar_wait_bounded(bars + 8 * C::B_QFULL, (seg_n - 1) & 1, a.err, kErrDrain);
+}
+
+// ---------------------------------------------------------------------------
+// Issuing warp
+// ---------------------------------------------------------------------------
+template <int D, bool kBf16>
+__device__ void issuer(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int lane) {
+  using C = Cfg<D>;
+  constexpr int T = C::T, NT = C::NT;
+  // a negative scale becomes positive with Q negated
+  const uint32_t idesc_qk = mma_idesc<kBf16>(kTileRows, T, false) | (a.scale_log2 < 0.f ? kIdescNegateA : 0u);
+  constexpr uint32_t kIdescPV = mma_idesc<kBf16>(kTileRows, D, true);
+  const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
+  const Segment *descs = reinterpret_cast<const Segment *>(smem + C::kDescOff);
+  int slot_n = 0, seg_n = 0;
+  int blk_n[2] = {0, 0};  // blocks whose scores buffer u has held
+  auto wait = [&](int bar, int n, int code) { return warp_wait_bounded(bars + 8 * bar, n & 1, a.err, code, lane); };
+
+  for (;;) {
+    const int d = seg_n % kDescs;
+    if (!wait(C::B_DFULL + d, seg_n / kDescs, kErrWaitQ)) return;
+    const Segment s = descs[d];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * (C::B_DEMPTY + d));
+    if (s.kind < 0) return;
+    const int t0 = s.it * NT * a.TQ;
+    const int tiles = min(NT, (s.qn - t0 + a.TQ - 1) / a.TQ);
+    const Span span = span_of<T>(a, s.L, s.qn, t0, min(t0 + NT * a.TQ, s.qn));
+    if (!wait(C::B_QFULL, seg_n, kErrWaitQ)) return;
+    tc_fence_after();
+
+    // S(tile t, buffer u) = Q_t K^T with K in ring slot sl
+    auto scores = [&](int t, int u, int sl) {
+      if (lane == 0) {
+        const uint32_t q = sbase + C::kQOff + t * C::kQBytes, k = sbase + sl * C::kSlotBytes;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(tmem + u * T, smem_desc(q + (kk / 4) * (kTileRows * 128) + (kk % 4) * 32, 16, 1024),
+                 smem_desc(k + (kk / 4) * (T * 128) + (kk % 4) * 32, 16, 1024), idesc_qk, kk > 0);
+        mma_commit(bars + 8 * (C::B_SFULL + u));
+      }
+      ++blk_n[u];
+    };
+    // O_t += P V over the 16-key steps [k0, k1) of the block in ring slot sl
+    auto values = [&](int t, int u, int sl, int k0, int k1, bool first) {
+      if (lane == 0) {
+        const uint32_t v = sbase + sl * C::kSlotBytes;
+        for (int kk = k0; kk < k1; ++kk)
+          mma_ts(tmem + C::kOCol + t * D, tmem + u * T + kk * 8, smem_desc(v + kk * 2048, T * 128, 1024), kIdescPV,
+                 !first || kk > k0);
+        mma_commit(bars + 8 * (C::B_OFULL + t));
+      }
+    };
+    auto release = [&](int sl) {
+      if (lane == 0) mma_commit(bars + 8 * (C::B_EMPTY + sl));
+    };
+
+    const int n = s.end - s.beg;
+    if (!wait(C::B_FULL + slot_n % C::kSlots, slot_n / C::kSlots, kErrWaitFull)) return;
+    tc_fence_after();
+    if constexpr (NT == 2) {
+      for (int t = 0; t < tiles; ++t) scores(t, t, slot_n % C::kSlots);
+    } else {
+      scores(0, (blk_n[0] + blk_n[1]) & 1, slot_n % C::kSlots);
+    }
+    release(slot_n % C::kSlots);
+    if (n == 1 && lane == 0) mma_commit(bars + 8 * C::B_QEMPTY);
+    ++slot_n;
+    for (int j = 0; j < n; ++j) {
+      const int vs = slot_n % C::kSlots, v_phase = slot_n / C::kSlots;
+      const int ks = (slot_n + 1) % C::kSlots, k_phase = (slot_n + 1) / C::kSlots;
+      const bool next = j + 1 < n;
+      // The block's keys that some query may see, in steps of 16; within
+      // them the values of hidden keys are zeroed, so that 0 * V stays 0
+      // whatever the cache holds there.
+      const int tok0 = span.block(s.beg + j) * T;
+      const int top = max(0, min(T, span.hi - tok0));              // keys [top, T) are hidden
+      const int g0 = max(0, min(T, max(a.sinks - tok0, 0)));       // and keys [g0, g1)
+      const int g1 = max(g0, min(top, span.low - tok0));
+      const int k0 = g0 == 0 ? g1 / 16 : 0, k1 = (top + 15) / 16;
+      if (!wait(C::B_FULL + vs, v_phase, kErrWaitFull)) return;
+      if (g1 > g0 || top % 16 != 0) {
+        const uint32_t v = sbase + vs * C::kSlotBytes;
+        for (int i = k0 * 16 * (D / 8) + lane; i < k1 * 16 * (D / 8); i += 32) {
+          const int key = i / (D / 8), c = i % (D / 8);
+          if (key >= top || (key >= g0 && key < g1))
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + (c / 8) * (T * 128) + key * 128 + (c % 8) * 16),
+                         "r"(0u) : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if constexpr (NT == 2) {
+        for (int t = 0; t < tiles; ++t) {
+          if (!wait(C::B_PREADY + t, blk_n[t] - 1, kErrWaitFull)) return;
+          tc_fence_after();
+          values(t, t, vs, k0, k1, j == 0);
+          if (next) {
+            if (t == 0) {
+              if (!wait(C::B_FULL + ks, k_phase, kErrWaitFull)) return;
+              tc_fence_after();
+            }
+            scores(t, t, ks);
+          }
+        }
+      } else {
+        const int u = (blk_n[0] + blk_n[1] - 1) & 1, nu = blk_n[u] - 1;  // this block's buffer and its use
+        if (next) {
+          if (!wait(C::B_FULL + ks, k_phase, kErrWaitFull)) return;
+          tc_fence_after();
+          scores(0, u ^ 1, ks);
+        }
+        if (!wait(C::B_PREADY + u, nu, kErrWaitFull)) return;
+        tc_fence_after();
+        values(0, u, vs, k0, k1, j == 0);
+      }
+      release(vs);
+      ++slot_n;
+      if (next) {
+        release(ks);
+        ++slot_n;
+        if (j + 2 == n && lane == 0) mma_commit(bars + 8 * C::B_QEMPTY);
+      }
+    }
+    ++seg_n;
+  }
+}
+
+// n ones from bit 0 up, for any n.
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// ---------------------------------------------------------------------------
+// Softmax warpgroups: thread r of warpgroup t owns row r of tile t.
+// ---------------------------------------------------------------------------
+template <int D, bool kBf16>
+__device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int t, int warp, int lane) {
+  using C = Cfg<D>;
+  constexpr int T = C::T, NT = C::NT;
+  const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
+  const Segment *descs = reinterpret_cast<const Segment *>(smem + C::kDescOff);
+  const int r = warp * 32 + lane;                        // row of the tile
+  const uint32_t lanes = (uint32_t)(warp * 32) << 16;    // this warp's lanes of tensor memory
+  const uint32_t o_addr = tmem + lanes + C::kOCol + t * D;
+  // The issuing warp has negated the scores for a negative scale.  A zero scale
+  // becomes one that leaves nothing of a score, since -inf marks a masked one.
+  const float sl2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
+  int seg_n = 0, blk_n = 0, o_n = 0;  // segments, score blocks, accumulations seen
+  auto wait = [&](int bar, int n, int code) { return warp_wait_bounded(bars + 8 * bar, n & 1, a.err, code, lane); };
+
+  for (;;) {
+    const int d = seg_n % kDescs;
+    if (!wait(C::B_DFULL + d, seg_n / kDescs, kErrWaitQ)) return;
+    const Segment s = descs[d];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * (C::B_DEMPTY + d));
+    ++seg_n;
+    if (s.kind < 0) return;
+    const int u0 = s.it * NT * a.TQ, tt0 = u0 + t * a.TQ;  // first token of the unit and of this tile
+    if (tt0 >= s.qn) continue;                              // the unit's second tile is empty
+    const Span span = span_of<T>(a, s.L, s.qn, u0, min(u0 + NT * a.TQ, s.qn));
+    const int tok = tt0 + r / a.G;
+    const bool real = r < a.TQ * a.G && tok < s.qn;
+    // keys this row sees: [0, sinks) and [low, lim)
+    int lim = a.causal ? min(s.L, s.L - s.qn + tok + 1) : s.L;
+    if (!real) lim = 0;
+    const int low = a.window > 0 ? max(lim - a.window, 0) : 0;
+    // a block needs the mask unless every row of the tile sees all of it
+    const int tile_lim = a.causal ? s.L - s.qn + tt0 + 1 : s.L;
+    const int tile_low = a.window > 0 ? s.L - s.qn + min(tt0 + a.TQ, s.qn) - a.window : 0;
+
+    float m = -INFINITY, l = 0.f;  // running maximum (base 2, scaled) and sum
+    for (int blk = s.beg; blk < s.end; ++blk) {
+      const int u = NT == 2 ? t : blk_n & 1, un = NT == 2 ? blk_n : blk_n >> 1;
+      if (!wait(C::B_SFULL + u, un, kErrWaitFull)) return;
+      tc_fence_after();
+      ++blk_n;
+      const uint32_t s_addr = tmem + lanes + u * T;
+      float x[T];
+#pragma unroll
+      for (int c = 0; c < T; c += 32) tmem_ld32(s_addr + c, reinterpret_cast<uint32_t *>(x + c));
+      tmem_wait_ld();
+      const int j0 = span.block(blk) * T;
+      if (j0 + T > tile_lim || (j0 < tile_low && j0 + T > a.sinks)) {
+#pragma unroll
+        for (int c = 0; c < T; c += 32) {  // one bit a key: seen or not
+          const int j = j0 + c;
+          const uint32_t seen = bits_below(lim - j) & (~bits_below(low - j) | bits_below(a.sinks - j));
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[c + i] = (seen >> i) & 1u ? x[c + i] : -INFINITY;
+        }
+      }
+      float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int i = 4; i < T; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+      // The reference m follows the maximum only once it is 2^8 behind, so
+      // the accumulator is hardly ever rescaled; weights stay below 2^8.
+      const bool behind = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
+      if (__any_sync(0xffffffffu, behind)) {
+        const float mn = fmaxf(m, top);
+        const float alpha = m == mn ? 1.f : ex2(m - mn);
+        m = mn;
+        l *= alpha;
+        if (blk > s.beg) {
+          if (!wait(C::B_OFULL + t, o_n - 1, kErrWaitFull)) return;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            tmem_ld16(o_addr + c, reinterpret_cast<uint32_t *>(o));
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= alpha;
+            tmem_st16(o_addr + c, reinterpret_cast<uint32_t *>(o));
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : -m;
+      const float2 sc = make_float2(sl2, sl2), bs = make_float2(base, base);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int c = 0; c < T; c += 32) {
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          float2 e = fma2(make_float2(x[c + i], x[c + i + 1]), sc, bs);
+          e.x = ex2(e.x);
+          e.y = ex2(e.y);
+          sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
+          p[i >> 1] = pack2<kBf16>(e.x, e.y);
+        }
+        tmem_st16(s_addr + (c >> 1), p);
+      }
+      sum[0] = add2(sum[0], sum[1]);
+      l += sum[0].x + sum[0].y;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bars + 8 * (C::B_PREADY + u));
+      ++o_n;
+    }
+
+    // ---- the rows: O / l and LSE ----
+    // With one tile the last scores were issued before the values of the
+    // block before, which may not be done: its phase is waited for first
+    // (a parity tells neighbouring phases apart, not the one before).
+    if (NT == 1 && o_n > 1 && !wait(C::B_OFULL + t, o_n - 2, kErrWaitFull)) return;
+    if (!wait(C::B_OFULL + t, o_n - 1, kErrWaitFull)) return;
+    tc_fence_after();
+    const float inv = 1.f / l;
+    const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    const int hq = s.h * a.G + r % a.G;
+    const size_t piece = s.kind == 0 ? 0 : (size_t)blockIdx.x * 2 + (s.kind - 1);
+    const size_t piece_row = piece * (NT * kTileRows) + t * kTileRows + r;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      float o[32];
+      tmem_ld32(o_addr + c, reinterpret_cast<uint32_t *>(o));
+      tmem_wait_ld();
+      if (real) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;  // no key: O holds nothing to read
+        if (s.kind == 0) {
+          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + ((size_t)(s.q0 + tok) * a.Hq + hq) * D + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_uint4(pack2<kBf16>(o[8 * i], o[8 * i + 1]), pack2<kBf16>(o[8 * i + 2], o[8 * i + 3]),
+                                pack2<kBf16>(o[8 * i + 4], o[8 * i + 5]), pack2<kBf16>(o[8 * i + 6], o[8 * i + 7]));
+        } else {
+          float4 *dst = reinterpret_cast<float4 *>(a.o_part + piece_row * D + c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      }
+      __syncwarp();
+    }
+    if (real) {
+      if (s.kind == 0) {
+        if (a.lse != nullptr) a.lse[(size_t)hq * a.total_q + s.q0 + tok] = lse;
+      } else {
+        a.lse_part[piece_row] = lse;
+      }
+    }
+    // the head piece's description, for the merge
+    if (s.kind == 1 && t == 0 && r == 0) {
+      PieceDesc &pd = a.pieces[blockIdx.x];
+      pd.q0 = s.q0;
+      pd.h = s.h;
+      pd.t0 = u0;
+      pd.tokens = min(NT * a.TQ, s.qn - u0);
+      pd.c_first = s.c_first;
+      pd.n_pieces = s.n_pieces;
+    }
+    tc_fence_before();  // the accumulator has been read before this thread's next arrival
+  }
+}
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+    prefill_kernel(const __grid_constant__ PrefillMaps tm, const __grid_constant__ PrefillArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t bars = smem_addr(smem) + C::kBarOff;
+  const uint32_t tmem_slot = bars + 8 * C::B_COUNT;
+  if ((smem_addr(smem) & 1023u) != 0) {  // the swizzle needs 1024-byte aligned slots
+    if (tid == 0) atomicOr(a.err, kErrAlign);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(bars + 8 * (C::B_FULL + i), 1);
+      mbar_init(bars + 8 * (C::B_EMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars + 8 * (C::B_SFULL + i), 1);
+      mbar_init(bars + 8 * (C::B_PREADY + i), kTileRows);
+      mbar_init(bars + 8 * (C::B_OFULL + i), 1);
+    }
+    mbar_init(bars + 8 * C::B_QFULL, 1);
+    mbar_init(bars + 8 * C::B_QEMPTY, 1);
+    for (int i = 0; i < kDescs; ++i) {
+      mbar_init(bars + 8 * (C::B_DFULL + i), 1);
+      mbar_init(bars + 8 * (C::B_DEMPTY + i), C::kSoftmaxWarps + 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == C::kMmaWarp) tmem_alloc(tmem_slot, 512);
+  grid_launch_dependents();
+  // Inputs may be written, and outputs and workspace used, by the kernel
+  // this launch depends on.
+  grid_dependency_wait();
+  // the rows' positions, for the producer's scan (the ring is still unused)
+  long long *rows = reinterpret_cast<long long *>(smem);
+  for (int b = warp; b < a.B; b += C::kThreads / 32) {
+    int q0, qn, L;
+    row_of(a, b, q0, qn, L);
+    const long long n = row_positions<D>(a, qn, L, lane);
+    if (lane == 0) {
+      rows[b] = n;
+      if (b % (int)gridDim.x == (int)blockIdx.x) check_row(a, b);
+    }
+  }
+  if (tid == 0) a.pieces[blockIdx.x].n_pieces = 0;  // until a head piece says otherwise
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  uint32_t tmem;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
+  if (warp >= C::kSoftmaxWarps) {
+    if constexpr (C::NT == 2) regs_dec<88>();  // 168 a thread at launch: 384 x 168 = 256 x 208 + 128 x 88
+    if (warp == C::kMmaWarp) issuer<D, kBf16>(a, smem, tmem, lane);
+    else if (warp == C::kProducerWarp) producer<D, kBf16>(tm, a, smem, lane);
+  } else {
+    if constexpr (C::NT == 2) regs_inc<208>();
+    softmax<D, kBf16>(a, smem, tmem, warp / 4, warp % 4, lane);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == C::kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// Merge of the units that ranges cut: cut i (between CTAs i - 1 and i) of a
+// unit with n pieces takes the (i - c_first)-th share of its rows, and
+// blockIdx.y a part of that.  LSE = ln sum exp(lse_p), O = sum exp(lse_p - LSE) O_p.
+// One warp a row.
+// ---------------------------------------------------------------------------
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ PrefillArgs a) {
+  constexpr int NT = Cfg<D>::NT;
+  constexpr float kLog2e = 1.4426950408889634f;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int cta = blockIdx.x + 1;
+  const PieceDesc pd = a.pieces[cta];
+  const int n = pd.n_pieces;
+  if (n < 2) return;
+  const int lane = threadIdx.x & 31;
+  const int rows = pd.tokens * a.G;
+  const int parts = (n - 1) * gridDim.y * 4;
+  const int part = ((cta - pd.c_first - 1) * gridDim.y + blockIdx.y) * 4 + (threadIdx.x >> 5);
+  const int beg = (int)((long long)rows * part / parts), end = (int)((long long)rows * (part + 1) / parts);
+  auto slot_of = [&](int i) -> size_t { return i == 0 ? (size_t)pd.c_first * 2 + 1 : (size_t)(pd.c_first + i) * 2; };
+  for (int m = beg; m < end; ++m) {
+    const int tok = m / a.G, g = m % a.G;
+    const int row = (tok / a.TQ) * kTileRows + (tok % a.TQ) * a.G + g;  // of the unit's tiles
+    float mx = -INFINITY;
+    for (int p = lane; p < n; p += 32) mx = fmaxf(mx, a.lse_part[slot_of(p) * (NT * kTileRows) + row] * kLog2e);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    float sum = 0.f;
+    if (mx != -INFINITY)
+      for (int p = lane; p < n; p += 32) sum += ex2(a.lse_part[slot_of(p) * (NT * kTileRows) + row] * kLog2e - mx);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float lse2 = sum > 0.f ? mx + log2f(sum) : -INFINITY;
+    const int hq = pd.h * a.G + g, token = pd.q0 + pd.t0 + tok;
+    if (lane == 0 && a.lse != nullptr) a.lse[(size_t)hq * a.total_q + token] = lse2 * kLn2;
+    for (int c = lane * 4; c < D; c += 128) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int p = 0; p < n; ++p) {
+        const size_t pr = slot_of(p) * (NT * kTileRows) + row;
+        const float lp = a.lse_part[pr];
+        const float wgt = lp == -INFINITY || lse2 == -INFINITY ? 0.f : ex2(lp * kLog2e - lse2);
+        const float4 v = *reinterpret_cast<const float4 *>(a.o_part + pr * D + c);
+        acc.x += wgt * v.x; acc.y += wgt * v.y; acc.z += wgt * v.z; acc.w += wgt * v.w;
+      }
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + ((size_t)token * a.Hq + hq) * D + c) =
+          make_uint2(pack2<kBf16>(acc.x, acc.y), pack2<kBf16>(acc.z, acc.w));
+    }
+  }
+}
+
+// 3-D map {D, Hq, tokens} of the packed queries; box {64, G, TQ}: one tile's
+// packed rows of one 64-column chunk, 128-byte swizzle.
+bool encode_q_map(CUtensorMap *m, const void *q, int D, int Hq, int total_q, int G, int TQ, bool bf16) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)total_q};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hq * D * 2};
+  cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)TQ};
+  cuuint32_t estride[3] = {1u, 1u, 1u};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(q),
+             dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kBf16>
+mxa_status_t launch_typed(const PrefillLaunch &L, PrefillArgs a, cudaStream_t stream) {
+  using C = Cfg<D>;
+  constexpr int kMaxDevices = 64;
+  static std::mutex mu;
+  static bool done[kMaxDevices] = {};
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return MXA_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    const bool known = device >= 0 && device < kMaxDevices;
+    if (!known || !done[device]) {
+      if (cudaFuncSetAttribute(prefill_kernel<D, kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+        return MXA_ERR_CUDA;
+      if (known) done[device] = true;
+    }
+  }
+  const mxa_decode_params_t &p = L.p;
+  // Boxes of whole 8-token groups of one page: the largest common divisor
+  // of the page and the block serves every page size that is a multiple of 8.
+  int box = C::T;
+  if (!a.contiguous)
+    while (p.page_size % box != 0) box /= 2;
+  a.box_tokens = box;
+  PrefillMaps tm;
+  const long long pool_tokens = (long long)(a.contiguous ? p.B : p.num_pages) * p.page_size;
+  if (!kv_maps(&tm.kv, L.k_cache, L.v_cache, D, p.Hkv, pool_tokens, box, kBf16) ||
+      !encode_q_map(&tm.q, L.q, D, p.Hq, L.total_q, a.G, a.TQ, kBf16))
+    return MXA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)L.plan.grid);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, prefill_kernel<D, kBf16>, tm, a) != cudaSuccess) return MXA_ERR_CUDA;
+  if (L.plan.grid > 1) {
+    cfg.gridDim = dim3((unsigned)(L.plan.grid - 1), 4);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    if (cudaLaunchKernelEx(&cfg, merge_kernel<D, kBf16>, a) != cudaSuccess) return MXA_ERR_CUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? MXA_OK : MXA_ERR_CUDA;
+}
+
+}  // namespace
+
+mxa_status_t launch_prefill(const PrefillLaunch &L, cudaStream_t stream) {
+  const mxa_decode_params_t &p = L.p;
+  PrefillArgs a{};
+  mxa_status_t st = device_error_word(&a.err);
+  if (st != MXA_OK) return st;
+  a.cu_q = L.cu_q;
+  a.seqlens = L.seqlens;
+  a.block_table = L.block_table;
+  a.out = L.out;
+  a.lse = L.lse;
+  uint8_t *ws = static_cast<uint8_t *>(L.workspace);
+  a.pieces = reinterpret_cast<PieceDesc *>(ws);
+  a.lse_part = reinterpret_cast<float *>(ws + L.plan.lse_off);
+  a.o_part = reinterpret_cast<float *>(ws + L.plan.o_off);
+  a.B = p.B;
+  a.Hq = p.Hq;
+  a.Hkv = p.Hkv;
+  a.G = p.Hq / p.Hkv;
+  a.TQ = kTileRows / a.G;
+  a.total_q = L.total_q;
+  a.max_q = p.q_len;
+  a.page_size = p.page_size;
+  a.num_pages = p.num_pages;
+  a.mpps = p.max_pages_per_seq;
+  a.contiguous = L.block_table == nullptr;
+  a.max_seqlen_k = p.max_seqlen_k;
+  a.causal = L.causal;
+  a.window = L.window < p.max_seqlen_k ? L.window : p.max_seqlen_k;  // a longer one hides nothing
+  a.sinks = L.window > 0 ? L.sinks : 0;
+  a.unit_cost = L.plan.unit_cost;
+  a.scale_log2 = L.scale * 1.4426950408889634f;
+  const bool bf16 = p.dtype == MXA_BF16;
+  if (p.D == 128) return bf16 ? launch_typed<128, true>(L, a, stream) : launch_typed<128, false>(L, a, stream);
+  if (p.D == 64) return bf16 ? launch_typed<64, true>(L, a, stream) : launch_typed<64, false>(L, a, stream);
+  return bf16 ? launch_typed<256, true>(L, a, stream) : launch_typed<256, false>(L, a, stream);
+}
+
+// One CTA per SM, and no more than the work can feed with two blocks each.
+PrefillPlan plan_prefill(const mxa_decode_params_t &p, int total_q, int sm_count) {
+  const int G = p.Hq / p.Hkv, NT = p.D <= 128 ? 2 : 1, T = p.D <= 128 ? 128 : 64, TQ = kTileRows / G;
+  PrefillPlan plan = {};
+  plan.unit_cost = 1;
+  // every row's last group may be partial
+  const long long groups = (long long)total_q / (NT * TQ) + (p.B < total_q ? p.B : total_q);
+  const long long blocks = ((long long)p.max_seqlen_k + T - 1) / T + 1;
+  const long long cap = groups * p.Hkv * ((blocks + 1) / 2);
+  plan.grid = (int)(cap < sm_count ? (cap < 1 ? 1 : cap) : sm_count);
+  plan.lse_off = align256(sizeof(PieceDesc) * (size_t)plan.grid);
+  const size_t rows = plan.grid > 1 ? (size_t)plan.grid * 2 * NT * kTileRows : 0;
+  plan.o_off = plan.lse_off + align256(rows * 4);
+  plan.workspace_bytes = plan.o_off + align256(rows * p.D * 4);
+  return plan;
+}
+
+}  // namespace mxa

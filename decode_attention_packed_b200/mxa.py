@@ -32,7 +32,7 @@ EXPORTED = ("mxa_status_string", "mxa_should_pack_gqa", "mxa_num_splits_heuristi
             "mxa_decode_fwd", "mxa_decode_fwd_with_plan", "mxa_combine", "mxa_device_error",
             "mxa_decode_fwd_noalloc", "mxa_decode_fwd_append", "mxa_decode_fwd_varlen",
             "mxa_decode_fwd_f32out", "mxa_decode_workspace_size", "mxa_plan_window", "mxa_decode_fwd_window",
-            "mxa_extend_tables", "mxa_cache_write")
+            "mxa_extend_tables", "mxa_cache_write", "mxa_prefill_fwd", "mxa_prefill_workspace_size")
 
 SIZE_MAX = ctypes.c_size_t(-1).value
 
@@ -95,6 +95,11 @@ _lib.mxa_decode_fwd_window.argtypes = [_P, _P, _P, _P, _P, _P, _P, ctypes.POINTE
                                        ctypes.c_float, _I, _I, ctypes.POINTER(mxa_plan_t), _P, ctypes.c_size_t,
                                        _P, _P, _P]
 _lib.mxa_decode_fwd_window.restype = _I
+_lib.mxa_prefill_fwd.argtypes = [_P, _P, _I, _P, _P, _P, _P, ctypes.POINTER(mxa_decode_params_t), ctypes.c_float,
+                                 _I, _I, _I, _P, ctypes.c_size_t, _P, _P, _P]
+_lib.mxa_prefill_fwd.restype = _I
+_lib.mxa_prefill_workspace_size.argtypes = [ctypes.POINTER(mxa_decode_params_t), _I]
+_lib.mxa_prefill_workspace_size.restype = ctypes.c_size_t
 _lib.mxa_extend_tables.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P]
 _lib.mxa_extend_tables.restype = _I
 _lib.mxa_cache_write.argtypes = [_P, _P, ctypes.c_longlong, ctypes.c_longlong, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P]
@@ -248,6 +253,22 @@ def mxa_decode_fwd_window(q, k_cache, v_cache, k_new, v_new, block_table, cache_
                                       _ptr(block_table), _ptr(cache_seqlens), ctypes.byref(params), float(scale),
                                       int(window), int(sinks), ctypes.byref(plan), _ptr(workspace), ws_bytes,
                                       _ptr(out), _ptr(lse), _stream(stream)), "mxa_decode_fwd_window")
+
+
+def mxa_prefill_workspace_size(params: mxa_decode_params_t, total_q: int) -> int:
+    """Workspace bytes of mxa_prefill_fwd; SIZE_MAX when refused."""
+    return int(_lib.mxa_prefill_workspace_size(ctypes.byref(params), int(total_q)))
+
+
+def mxa_prefill_fwd(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, params, scale, causal, window,
+                    sinks, workspace, out, lse, stream=None) -> None:
+    """Attention of packed chunks q [total_q, Hq, D] over the cache; params.q_len
+    bounds every row's queries (see mxa.h)."""
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.mxa_prefill_fwd(_ptr(q), _ptr(cu_seqlens_q), q.shape[0], _ptr(k_cache), _ptr(v_cache),
+                                _ptr(block_table), _ptr(cache_seqlens), ctypes.byref(params), float(scale),
+                                int(causal), int(window), int(sinks), _ptr(workspace), ws_bytes, _ptr(out),
+                                _ptr(lse), _stream(stream)), "mxa_prefill_fwd")
 
 
 def mxa_extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, page_size, num_pages, slots,
@@ -410,8 +431,59 @@ def decode_varlen(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens,
 
 
 # --------------------------------------------------------------------------
-# the cache's bookkeeping
+# chunks of new tokens, and the cache's bookkeeping
 # --------------------------------------------------------------------------
+
+def prepare_prefill(q, cu_seqlens_q, k_cache, block_table, *, max_seqlen_q, max_seqlen_k=None) -> Prepared:
+    """The workspace of prefill calls with up to q.shape[0] packed tokens, for
+    a serving loop to keep."""
+    total_q, Hq, D = q.shape
+    B = cu_seqlens_q.shape[0] - 1
+    shape = torch.empty((B, int(max_seqlen_q), Hq, D), dtype=q.dtype, device="meta")
+    params = params_for(shape, k_cache, block_table, max_seqlen_k)
+    size = mxa_prefill_workspace_size(params, total_q)
+    if size == SIZE_MAX:  # the run call names the reason
+        size = 0
+    return Prepared(params, None, torch.empty(size, dtype=torch.uint8, device=q.device))
+
+
+def prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, max_seqlen_q, scale=None, causal=True,
+            window=0, sinks=0, max_seqlen_k=None, out=None, lse=None, prepared: Optional[Prepared] = None,
+            return_lse=True, stream=None):
+    """out [total_q, Hq, D] (and lse [Hq, total_q] fp32) for chunks of new
+    tokens over the cache, which holds their keys and values already:
+    q [total_q, Hq, D], row b's tokens at cu_seqlens_q[b] .. cu_seqlens_q[b + 1]
+    - 1, its last ones among cache_seqlens[b] keys; max_seqlen_q >= every
+    row's count.  Rows of one token and of thousands may be mixed.
+
+    causal: a token sees the keys up to its own position.  window > 0 (causal
+    only) leaves it its last `window` keys and the first `sinks` keys."""
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    if prepared is None:
+        prepared = prepare_prefill(q, cu_seqlens_q, k_cache, block_table, max_seqlen_q=max_seqlen_q,
+                                   max_seqlen_k=max_seqlen_k)
+        if stream is not None and not isinstance(stream, int):
+            prepared.workspace.record_stream(stream)
+    _want(q, "q", q.dtype)
+    _want(k_cache, "k_cache", q.dtype)
+    _want(v_cache, "v_cache", q.dtype, k_cache.shape)
+    _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, (prepared.params.B + 1,))
+    _want(cache_seqlens, "cache_seqlens", torch.int32, (prepared.params.B,))
+    if block_table is not None:
+        _want(block_table, "block_table", torch.int32, (prepared.params.B, prepared.params.max_pages_per_seq))
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _want(out, "out", q.dtype, q.shape)
+    if lse is None and return_lse:
+        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    elif lse is not None:
+        _want(lse, "lse", torch.float32, (q.shape[1], q.shape[0]))
+    mxa_prefill_fwd(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, prepared.params, scale, causal,
+                    window, sinks, prepared.workspace, out, lse, stream)
+    return out, lse
+
 
 def _want_here(t: torch.Tensor, name: str) -> None:
     if not t.is_cuda or t.get_device() != torch.cuda.current_device():

@@ -305,6 +305,40 @@ MXA_API mxa_status_t mxa_decode_fwd_window(const void *q, void *k_cache, void *v
                                            void *workspace, size_t workspace_bytes, void *out, float *lse,
                                            void *stream);
 
+/* Attention of chunks of new tokens over the cache (prefill, chunked prefill,
+ * and batches that mix chunks with single tokens): the operation and layouts
+ * of mxa_decode_fwd_varlen, for any number of queries a row.
+ *   q, cu_seqlens_q, total_q, out, lse: as there (q and out [total_q, Hq, D],
+ *            lse [Hq, total_q] or NULL); the keys and values of the new tokens are
+ *            in the cache already (mxa_cache_write), L_b counts them
+ *   params : q_len bounds every row's queries; Hq / Hkv <= 128; B <= 12288; a
+ *            paged cache needs a page_size that is a multiple of 8, a contiguous
+ *            one (block_table NULL) any row capacity >= max_seqlen_k
+ *   causal : 0: every query sees L_b keys; 1: query t of a row with n_b
+ *            queries is at position p = L_b - n_b + t and sees the keys j <= p
+ *   window, sinks : window 0: none.  window >= 1 (causal only): j <= p and
+ *            (j > p - window or j < sinks); pages whose keys no query of a row
+ *            sees are not read (see mxa_decode_fwd_window)
+ *   workspace : mxa_prefill_workspace_size(params, total_q) bytes, 256-byte
+ *            aligned; contents on entry are ignored; calls that may overlap
+ *            need one each
+ * A query that sees no key gets O = 0 and LSE = -inf.  Weights enter the
+ * product with V rounded once to the input type; sums, maxima and
+ * accumulators are float32.
+ * Device-side breaches (lengths, offsets, page ids) are confined and reported
+ * as for mxa_decode_fwd_varlen.  Errors: MXA_ERR_INVALID_ARG,
+ * MXA_ERR_UNSUPPORTED, MXA_ERR_WORKSPACE, MXA_ERR_CUDA. */
+MXA_API mxa_status_t mxa_prefill_fwd(const void *q, const int32_t *cu_seqlens_q, int total_q, const void *k_cache,
+                                     const void *v_cache, const int32_t *block_table,
+                                     const int32_t *cache_seqlens, const mxa_decode_params_t *params, float scale,
+                                     int causal, int window, int sinks, void *workspace, size_t workspace_bytes,
+                                     void *out, float *lse, void *stream);
+
+/* Bytes of workspace for mxa_prefill_fwd with these params and total_q
+ * queries on the current device (never less for more queries); SIZE_MAX when
+ * the shape is refused or no device can be queried. */
+MXA_API size_t mxa_prefill_workspace_size(const mxa_decode_params_t *params, int total_q);
+
 /* Pages and cache slots for a step's new tokens, on the device: row b holds
  * L_b keys in its first ceil(L_b / page_size) pages and receives
  * n_b = cu_seqlens_q[b + 1] - cu_seqlens_q[b] new tokens.
