@@ -5,8 +5,8 @@
 //
 // Each CTA walks a contiguous share of the work with three roles:
 //  - a producer warp finds the CTA's share, gathers K and V pages through the
-//    block table with TMA into a ring of shared-memory slots, and loads the
-//    packed query rows;
+//    block table with TMA into a ring of shared-memory slots; a query warp
+//    loads the packed query rows;
 //  - an issuing warp runs S = Q K^T and O += P V on the tensor cores
 //    (tcgen05, accumulators and P in tensor memory);
 //  - one or two softmax warpgroups, one thread per packed query row, turn S
@@ -47,7 +47,7 @@ struct Cfg {
   static constexpr int T = D <= 128 ? 128 : 64;     // keys of a block
   static constexpr int CH = D / 64;                 // 64-column chunks of a row
   static constexpr int kSoftmaxWarps = 4 * NT;
-  static constexpr int kMmaWarp = kSoftmaxWarps, kProducerWarp = kSoftmaxWarps + 1;
+  static constexpr int kMmaWarp = kSoftmaxWarps, kProducerWarp = kSoftmaxWarps + 1, kQueryWarp = kSoftmaxWarps + 2;
   static constexpr int kThreads = 128 * (NT + 1);
   static constexpr int kSlotBytes = T * D * 2;      // one block of K or of V
   static constexpr int kSlots = 160 * 1024 / kSlotBytes;
@@ -265,13 +265,12 @@ __device__ Walk walk_start(const PrefillArgs &a, long long *rows, int lane) {
 template <int D, bool kBf16>
 __device__ void producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *smem, int lane) {
   using C = Cfg<D>;
-  constexpr int T = C::T, NT = C::NT;
+  constexpr int T = C::T;
   const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
   Segment *descs = reinterpret_cast<Segment *>(smem + C::kDescOff);
   if (lane == 0) {
     prefetch_tmap(&tm.kv.k);
     prefetch_tmap(&tm.kv.v);
-    prefetch_tmap(&tm.q);
   }
   Walk w = walk_start<D>(a, reinterpret_cast<long long *>(smem), lane);
   fence_proxy_async_smem();  // the scan's accesses precede the ring's loads
@@ -301,20 +300,6 @@ __device__ void producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *s
     }
     __syncwarp();
     if (!more) break;
-    // queries: free once the unit before has issued its last scores
-    if (!warp_wait_bounded(bars + 8 * C::B_QEMPTY, (seg_n & 1) ^ 1, a.err, kErrWaitQ, lane)) {
-      ok = false;
-      break;
-    }
-    const int t0 = s.it * NT * a.TQ;
-    const int tiles = min(NT, (s.qn - t0 + a.TQ - 1) / a.TQ);
-    if (lane == 0) mbar_arrive_expect_tx(bars + 8 * C::B_QFULL, (uint32_t)(tiles * C::CH * a.TQ * a.G * 128));
-    __syncwarp();
-    if (lane < tiles * C::CH) {
-      const int t = lane / C::CH, ch = lane % C::CH;
-      tma_load_3d(sbase + C::kQOff + t * C::kQBytes + ch * (kTileRows * 128), &tm.q, ch * 64, s.h * a.G,
-                  s.q0 + t0 + t * a.TQ, bars + 8 * C::B_QFULL);
-    }
     ++seg_n;
     const Span span = walk_span<D>(a, at);
     int page = 0;
@@ -365,132 +350,168 @@ __device__ void producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *s
   // Leave only when the copies issued here have landed.
   for (int j = max(0, slot_n - C::kSlots); j < slot_n; ++j)
     mbar_wait_bounded(bars + 8 * (C::B_FULL + j % C::kSlots), (j / C::kSlots) & 1, a.err, kErrDrain);
-  if (seg_n > 0) mbar_wait_bounded(bars + 8 * C::B_QFULL, (seg_n - 1) & 1, a.err, kErrDrain);
 }
 
 // ---------------------------------------------------------------------------
-// Issuing warp
+// Query warp: a unit's packed rows, as soon as the unit before has issued its
+// last scores.  A warp of its own, so that the next unit's first keys and
+// values are on their way before that.
 // ---------------------------------------------------------------------------
-template <int D, bool kBf16>
-__device__ void issuer(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int lane) {
+template <int D>
+__device__ void queries(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *smem, int lane) {
   using C = Cfg<D>;
-  constexpr int T = C::T, NT = C::NT;
-  // a negative scale becomes positive with Q negated
-  const uint32_t idesc_qk = mma_idesc<kBf16>(kTileRows, T, false) | (a.scale_log2 < 0.f ? kIdescNegateA : 0u);
-  constexpr uint32_t kIdescPV = mma_idesc<kBf16>(kTileRows, D, true);
+  constexpr int NT = C::NT;
   const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
   const Segment *descs = reinterpret_cast<const Segment *>(smem + C::kDescOff);
-  int slot_n = 0, seg_n = 0;
-  int blk_n[2] = {0, 0};  // blocks whose scores buffer u has held
-  auto wait = [&](int bar, int n, int code) { return warp_wait_bounded(bars + 8 * bar, n & 1, a.err, code, lane); };
-
-  for (;;) {
+  if (lane == 0) prefetch_tmap(&tm.q);
+  int seg_n = 0;
+  for (;; ++seg_n) {
     const int d = seg_n % kDescs;
-    if (!wait(C::B_DFULL + d, seg_n / kDescs, kErrWaitQ)) return;
+    if (!warp_wait_bounded(bars + 8 * (C::B_DFULL + d), (seg_n / kDescs) & 1, a.err, kErrWaitQ, lane)) break;
     const Segment s = descs[d];
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * (C::B_DEMPTY + d));
+    if (s.kind < 0) break;
+    if (!warp_wait_bounded(bars + 8 * C::B_QEMPTY, (seg_n & 1) ^ 1, a.err, kErrWaitQ, lane)) break;
+    const int t0 = s.it * NT * a.TQ;
+    const int tiles = min(NT, (s.qn - t0 + a.TQ - 1) / a.TQ);
+    if (lane == 0) mbar_arrive_expect_tx(bars + 8 * C::B_QFULL, (uint32_t)(tiles * C::CH * a.TQ * a.G * 128));
+    __syncwarp();
+    if (lane < tiles * C::CH) {
+      const int t = lane / C::CH, ch = lane % C::CH;
+      tma_load_3d(sbase + C::kQOff + t * C::kQBytes + ch * (kTileRows * 128), &tm.q, ch * 64, s.h * a.G,
+                  s.q0 + t0 + t * a.TQ, bars + 8 * C::B_QFULL);
+    }
+  }
+  // leave only when the copies issued here have landed
+  if (seg_n > 0) mbar_wait_bounded(bars + 8 * C::B_QFULL, (seg_n - 1) & 1, a.err, kErrDrain);
+}
+
+// Keys of the block at tok0 that some query of the unit may see, as the
+// 16-key steps [k0, k1) of the product with V; hidden keys inside them, [top,
+// ..) and [g0, g1), get zeros for values, so that 0 * V stays 0 whatever the
+// cache holds there.
+struct Steps {
+  int top, g0, g1, k0, k1;
+  bool clear;
+};
+template <int T>
+__device__ __forceinline__ Steps steps_of(const PrefillArgs &a, const Span &span, int tok0) {
+  Steps s;
+  s.top = max(0, min(T, span.hi - tok0));
+  s.g0 = max(0, min(T, a.sinks - tok0));
+  s.g1 = max(s.g0, min(s.top, span.low - tok0));
+  s.k0 = s.g0 == 0 ? s.g1 / 16 : 0;
+  s.k1 = (s.top + 15) / 16;
+  s.clear = s.g1 > s.g0 || s.top % 16 != 0;
+  return s;
+}
+
+// ---------------------------------------------------------------------------
+// Issuing thread.  Its instructions between two products are what the tensor
+// cores wait for, so one lane runs the whole role: no warp-wide votes, and
+// operand descriptors stepped by additions.
+// ---------------------------------------------------------------------------
+template <int D, bool kBf16>
+__device__ void issuer(const PrefillArgs &a, uint8_t *smem, uint32_t tmem) {
+  using C = Cfg<D>;
+  constexpr int T = C::T, NT = C::NT;
+  constexpr uint32_t kHi = smem_desc_hi(1024);
+  constexpr uint32_t kIdescPV = mma_idesc<kBf16>(kTileRows, D, true);
+  // a negative scale becomes positive with Q negated
+  const uint32_t idesc_qk = mma_idesc<kBf16>(kTileRows, T, false) | (a.scale_log2 < 0.f ? kIdescNegateA : 0u);
+  const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
+  const Segment *descs = reinterpret_cast<const Segment *>(smem + C::kDescOff);
+  const uint32_t q_lo = smem_desc_lo(sbase + C::kQOff, 16);
+  int seg_n = 0;
+  int slot = 0, phase = 0;    // next ring slot and its phase
+  int blk_n[2] = {0, 0};      // blocks whose scores buffer u has held
+  auto wait = [&](int bar, int n, int code) { return mbar_wait_bounded(bars + 8 * bar, n & 1, a.err, code); };
+  auto advance = [&](int &sl, int &ph) {
+    if (++sl == C::kSlots) {
+      sl = 0;
+      ph ^= 1;
+    }
+  };
+  // S(tile t, buffer u) = Q_t K^T with K in ring slot sl
+  auto scores = [&](int t, int u, int sl) {
+    const uint32_t q = q_lo + t * (C::kQBytes / 16), k = smem_desc_lo(sbase + sl * C::kSlotBytes, 16);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+      mma_ss<kHi>(tmem + u * T, q + (kk / 4) * (kTileRows * 8) + (kk % 4) * 2, k + (kk / 4) * (T * 8) + (kk % 4) * 2,
+                  idesc_qk, kk > 0);
+    mma_commit(bars + 8 * (C::B_SFULL + u));
+    ++blk_n[u];
+  };
+  // O_t += P V over the 16-key steps [k0, k1) of the block in ring slot sl
+  auto values = [&](int t, int u, int sl, int k0, int k1, bool first) {
+    const uint32_t v = smem_desc_lo(sbase + sl * C::kSlotBytes, T * 128), o = tmem + C::kOCol + t * D, p = tmem + u * T;
+    if (k0 == 0 && k1 == T / 16) {
+#pragma unroll
+      for (int kk = 0; kk < T / 16; ++kk) mma_ts<kHi>(o, p + kk * 8, v + kk * 128, kIdescPV, kk > 0 || !first);
+    } else {
+      for (int kk = k0; kk < k1; ++kk) mma_ts<kHi>(o, p + kk * 8, v + kk * 128, kIdescPV, kk > k0 || !first);
+    }
+  };
+
+  for (;; ++seg_n) {
+    const int d = seg_n % kDescs;
+    if (!wait(C::B_DFULL + d, seg_n / kDescs, kErrWaitQ)) return;
+    const Segment s = descs[d];
+    mbar_arrive(bars + 8 * (C::B_DEMPTY + d));
     if (s.kind < 0) return;
     const int t0 = s.it * NT * a.TQ;
     const int tiles = min(NT, (s.qn - t0 + a.TQ - 1) / a.TQ);
     const Span span = span_of<T>(a, s.L, s.qn, t0, min(t0 + NT * a.TQ, s.qn));
-    if (!wait(C::B_QFULL, seg_n, kErrWaitQ)) return;
-    tc_fence_after();
-
-    // S(tile t, buffer u) = Q_t K^T with K in ring slot sl
-    auto scores = [&](int t, int u, int sl) {
-      if (lane == 0) {
-        const uint32_t q = sbase + C::kQOff + t * C::kQBytes, k = sbase + sl * C::kSlotBytes;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + u * T, smem_desc(q + (kk / 4) * (kTileRows * 128) + (kk % 4) * 32, 16, 1024),
-                 smem_desc(k + (kk / 4) * (T * 128) + (kk % 4) * 32, 16, 1024), idesc_qk, kk > 0);
-        mma_commit(bars + 8 * (C::B_SFULL + u));
-      }
-      ++blk_n[u];
-    };
-    // O_t += P V over the 16-key steps [k0, k1) of the block in ring slot sl
-    auto values = [&](int t, int u, int sl, int k0, int k1, bool first) {
-      if (lane == 0) {
-        const uint32_t v = sbase + sl * C::kSlotBytes;
-        for (int kk = k0; kk < k1; ++kk)
-          mma_ts(tmem + C::kOCol + t * D, tmem + u * T + kk * 8, smem_desc(v + kk * 2048, T * 128, 1024), kIdescPV,
-                 !first || kk > k0);
-        mma_commit(bars + 8 * (C::B_OFULL + t));
-      }
-    };
-    auto release = [&](int sl) {
-      if (lane == 0) mma_commit(bars + 8 * (C::B_EMPTY + sl));
-    };
-
     const int n = s.end - s.beg;
-    if (!wait(C::B_FULL + slot_n % C::kSlots, slot_n / C::kSlots, kErrWaitFull)) return;
-    tc_fence_after();
+    if (!wait(C::B_QFULL, seg_n, kErrWaitQ)) return;
+    if (!wait(C::B_FULL + slot, phase, kErrWaitFull)) return;
     if constexpr (NT == 2) {
-      for (int t = 0; t < tiles; ++t) scores(t, t, slot_n % C::kSlots);
+      for (int t = 0; t < tiles; ++t) scores(t, t, slot);
     } else {
-      scores(0, (blk_n[0] + blk_n[1]) & 1, slot_n % C::kSlots);
+      scores(0, (blk_n[0] + blk_n[1]) & 1, slot);
     }
-    release(slot_n % C::kSlots);
-    if (n == 1 && lane == 0) mma_commit(bars + 8 * C::B_QEMPTY);
-    ++slot_n;
+    mma_commit(bars + 8 * (C::B_EMPTY + slot));
+    if (n == 1) mma_commit(bars + 8 * C::B_QEMPTY);
+    advance(slot, phase);
     for (int j = 0; j < n; ++j) {
-      const int vs = slot_n % C::kSlots, v_phase = slot_n / C::kSlots;
-      const int ks = (slot_n + 1) % C::kSlots, k_phase = (slot_n + 1) / C::kSlots;
       const bool next = j + 1 < n;
-      // The block's keys that some query may see, in steps of 16; within
-      // them the values of hidden keys are zeroed, so that 0 * V stays 0
-      // whatever the cache holds there.
-      const int tok0 = span.block(s.beg + j) * T;
-      const int top = max(0, min(T, span.hi - tok0));              // keys [top, T) are hidden
-      const int g0 = max(0, min(T, max(a.sinks - tok0, 0)));       // and keys [g0, g1)
-      const int g1 = max(g0, min(top, span.low - tok0));
-      const int k0 = g0 == 0 ? g1 / 16 : 0, k1 = (top + 15) / 16;
+      const int vs = slot, v_phase = phase;
+      advance(slot, phase);
+      const int ks = slot, k_phase = phase;
+      const Steps st = steps_of<T>(a, span, span.block(s.beg + j) * T);
       if (!wait(C::B_FULL + vs, v_phase, kErrWaitFull)) return;
-      if (g1 > g0 || top % 16 != 0) {
-        const uint32_t v = sbase + vs * C::kSlotBytes;
-        for (int i = k0 * 16 * (D / 8) + lane; i < k1 * 16 * (D / 8); i += 32) {
-          const int key = i / (D / 8), c = i % (D / 8);
-          if (key >= top || (key >= g0 && key < g1))
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + (c / 8) * (T * 128) + key * 128 + (c % 8) * 16),
-                         "r"(0u) : "memory");
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
       if constexpr (NT == 2) {
         for (int t = 0; t < tiles; ++t) {
           if (!wait(C::B_PREADY + t, blk_n[t] - 1, kErrWaitFull)) return;
           tc_fence_after();
-          values(t, t, vs, k0, k1, j == 0);
+          values(t, t, vs, st.k0, st.k1, j == 0);
           if (next) {
-            if (t == 0) {
-              if (!wait(C::B_FULL + ks, k_phase, kErrWaitFull)) return;
-              tc_fence_after();
-            }
+            if (t == 0 && !wait(C::B_FULL + ks, k_phase, kErrWaitFull)) return;
             scores(t, t, ks);
+          } else {
+            mma_commit(bars + 8 * (C::B_OFULL + t));
           }
         }
       } else {
         const int u = (blk_n[0] + blk_n[1] - 1) & 1, nu = blk_n[u] - 1;  // this block's buffer and its use
         if (next) {
           if (!wait(C::B_FULL + ks, k_phase, kErrWaitFull)) return;
-          tc_fence_after();
           scores(0, u ^ 1, ks);
+          mma_commit(bars + 8 * (C::B_EMPTY + ks));
         }
         if (!wait(C::B_PREADY + u, nu, kErrWaitFull)) return;
         tc_fence_after();
-        values(0, u, vs, k0, k1, j == 0);
+        values(0, u, vs, st.k0, st.k1, j == 0);
+        mma_commit(bars + 8 * C::B_OFULL);
       }
-      release(vs);
-      ++slot_n;
+      mma_commit(bars + 8 * (C::B_EMPTY + vs));
       if (next) {
-        release(ks);
-        ++slot_n;
-        if (j + 2 == n && lane == 0) mma_commit(bars + 8 * C::B_QEMPTY);
+        if (NT == 2) mma_commit(bars + 8 * (C::B_EMPTY + ks));
+        if (j + 2 == n) mma_commit(bars + 8 * C::B_QEMPTY);
+        advance(slot, phase);
       }
     }
-    ++seg_n;
   }
 }
 
@@ -514,7 +535,9 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
   // The issuing warp has negated the scores for a negative scale.  A zero scale
   // becomes one that leaves nothing of a score, since -inf marks a masked one.
   const float sl2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
-  int seg_n = 0, blk_n = 0, o_n = 0;  // segments, score blocks, accumulations seen
+  int seg_n = 0, blk_n = 0;   // segments and score blocks seen
+  int o_n = 0;                // uses of this tile's accumulator barrier (below)
+  int slot_n = 1;             // ring slot, of all so far, that holds the current block's values
   auto wait = [&](int bar, int n, int code) { return warp_wait_bounded(bars + 8 * bar, n & 1, a.err, code, lane); };
 
   for (;;) {
@@ -526,7 +549,10 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     ++seg_n;
     if (s.kind < 0) return;
     const int u0 = s.it * NT * a.TQ, tt0 = u0 + t * a.TQ;  // first token of the unit and of this tile
-    if (tt0 >= s.qn) continue;                              // the unit's second tile is empty
+    if (tt0 >= s.qn) {                                      // the unit's second tile is empty
+      slot_n += 2 * (s.end - s.beg);
+      continue;
+    }
     const Span span = span_of<T>(a, s.L, s.qn, u0, min(u0 + NT * a.TQ, s.qn));
     const int tok = tt0 + r / a.G;
     const bool real = r < a.TQ * a.G && tok < s.qn;
@@ -572,7 +598,9 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
         m = mn;
         l *= alpha;
         if (blk > s.beg) {
-          if (!wait(C::B_OFULL + t, o_n - 1, kErrWaitFull)) return;
+          // These scores were issued after the values of the block before
+          // (two tiles), or are waited for apart from them (one tile).
+          if (NT == 1 && !wait(C::B_OFULL, o_n - 1, kErrWaitFull)) return;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
@@ -603,17 +631,35 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
       }
       sum[0] = add2(sum[0], sum[1]);
       l += sum[0].x + sum[0].y;
+      if (t == 0) {
+        const Steps st = steps_of<T>(a, span, j0);
+        if (st.clear) {  // the row's last block, or one at the window's start: values of hidden keys become zeros
+          const int sl = slot_n % C::kSlots;
+          if (!wait(C::B_FULL + sl, slot_n / C::kSlots, kErrWaitFull)) return;
+          const uint32_t v = sbase + sl * C::kSlotBytes;
+          for (int i = st.k0 * 16 * (D / 8) + r; i < st.k1 * 16 * (D / 8); i += kTileRows) {
+            const int key = i / (D / 8), c = i % (D / 8);
+            if (key >= st.top || (key >= st.g0 && key < st.g1))
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + (c / 8) * (T * 128) + key * 128 + (c % 8) * 16),
+                           "r"(0u) : "memory");
+          }
+          fence_proxy_async_smem();  // before the product reads them
+          __syncwarp();
+        }
+        slot_n += 2;
+      }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(bars + 8 * (C::B_PREADY + u));
-      ++o_n;
+      if (NT == 1) ++o_n;
     }
 
     // ---- the rows: O / l and LSE ----
     // With one tile the last scores were issued before the values of the
     // block before, which may not be done: its phase is waited for first
     // (a parity tells neighbouring phases apart, not the one before).
-    if (NT == 1 && o_n > 1 && !wait(C::B_OFULL + t, o_n - 2, kErrWaitFull)) return;
+    if (NT == 1 && o_n > 1 && !wait(C::B_OFULL, o_n - 2, kErrWaitFull)) return;
+    if (NT == 2) ++o_n;  // once a unit; with one tile, once a block
     if (!wait(C::B_OFULL + t, o_n - 1, kErrWaitFull)) return;
     tc_fence_after();
     const float inv = 1.f / l;
@@ -690,7 +736,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     mbar_init(bars + 8 * C::B_QEMPTY, 1);
     for (int i = 0; i < kDescs; ++i) {
       mbar_init(bars + 8 * (C::B_DFULL + i), 1);
-      mbar_init(bars + 8 * (C::B_DEMPTY + i), C::kSoftmaxWarps + 1);
+      mbar_init(bars + 8 * (C::B_DEMPTY + i), C::kSoftmaxWarps + 2);
     }
     fence_mbar_init();
   }
@@ -719,8 +765,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
   if (warp >= C::kSoftmaxWarps) {
     if constexpr (C::NT == 2) regs_dec<88>();  // 168 a thread at launch: 384 x 168 = 256 x 208 + 128 x 88
-    if (warp == C::kMmaWarp) issuer<D, kBf16>(a, smem, tmem, lane);
-    else if (warp == C::kProducerWarp) producer<D, kBf16>(tm, a, smem, lane);
+    if (warp == C::kMmaWarp) {
+      if (lane == 0) issuer<D, kBf16>(a, smem, tmem);
+      __syncwarp();
+    } else if (warp == C::kProducerWarp) producer<D, kBf16>(tm, a, smem, lane);
+    else if (warp == C::kQueryWarp) queries<D>(tm, a, smem, lane);
   } else {
     if constexpr (C::NT == 2) regs_inc<208>();
     softmax<D, kBf16>(a, smem, tmem, warp / 4, warp % 4, lane);
