@@ -50,18 +50,24 @@ struct Cfg {
   static constexpr int kMmaWarp = kSoftmaxWarps, kProducerWarp = kSoftmaxWarps + 1, kQueryWarp = kSoftmaxWarps + 2;
   static constexpr int kThreads = 128 * (NT + 1);
   static constexpr int kSlotBytes = T * D * 2;      // one block of K or of V
-  static constexpr int kSlots = 160 * 1024 / kSlotBytes;
+  static constexpr int kSlots = 128 * 1024 / kSlotBytes;
   static constexpr int kQBytes = kTileRows * D * 2;
-  // tensor memory: two score buffers of T columns (P over the first half of
-  // each), then the tiles' accumulators
-  static constexpr int kOCol = 256;
+  // Tensor memory: NS score buffers of T columns, two weight buffers of T / 2
+  // (a column holds two weights of a row), then the tiles' accumulators.  At
+  // D = 128 the two tiles' scores take turns in one buffer: it is free again
+  // as soon as they are in registers.
+  static constexpr int NS = D == 128 ? 1 : 2;
+  static constexpr int kPCol = NS * T, kOCol = 512 - NT * D;
+  static_assert(kPCol + T <= kOCol, "tensor memory");
   // shared memory
   static constexpr int kQOff = kSlots * kSlotBytes;
-  static constexpr int kDescOff = kQOff + NT * kQBytes;
+  static constexpr int kStageOff = kQOff + NT * kQBytes;  // 4 KB a softmax warp, for the rows it writes out
+  static constexpr int kDescOff = kStageOff + kSoftmaxWarps * 4096;
   static constexpr int kBarOff = kDescOff + kDescs * 64;
   static constexpr int kSmem = kBarOff + 512;
   // barriers
-  static constexpr int B_FULL = 0, B_EMPTY = kSlots, B_SFULL = 2 * kSlots, B_PREADY = B_SFULL + 2;
+  static constexpr int B_FULL = 0, B_EMPTY = kSlots, B_SFULL = 2 * kSlots, B_SFREE = B_SFULL + 2;
+  static constexpr int B_PREADY = B_SFREE + 2;
   static constexpr int B_OFULL = B_PREADY + 2, B_QFULL = B_OFULL + 2, B_QEMPTY = B_QFULL + 1;
   static constexpr int B_DFULL = B_QEMPTY + 1, B_DEMPTY = B_DFULL + kDescs, B_COUNT = B_DEMPTY + kDescs;
   static_assert(B_COUNT * 8 + 16 <= 512 && kSmem <= 227 * 1024, "shared memory");
@@ -122,7 +128,7 @@ struct Walk {
   int b, h, it, tiles;
   int q0, qn, L;
   int blk, nb;
-  long long x, end, per_cta;
+  int x, end, per_cta;
 };
 
 template <int D>
@@ -137,16 +143,15 @@ __device__ __forceinline__ Span walk_span(const PrefillArgs &a, const Walk &w) {
 template <int D>
 __device__ Segment walk_take(const PrefillArgs &a, Walk &w) {
   Segment s;
-  const long long room = w.end - w.x;
-  const int len = (int)min((long long)(w.nb - w.blk), room);
+  const int len = min(w.nb - w.blk, w.end - w.x);
   s.b = w.b; s.h = w.h; s.it = w.it;
   s.q0 = w.q0; s.qn = w.qn; s.L = w.L;
   s.beg = w.blk;
   s.end = w.blk + len;
   s.kind = (s.beg == 0 && s.end == w.nb) ? 0 : s.beg > 0 ? 1 : 2;
-  const long long xs = w.x - w.blk;
-  s.c_first = (int)(xs / w.per_cta);
-  s.n_pieces = (int)((xs + w.nb - 1) / w.per_cta) - s.c_first + 1;
+  const int xs = w.x - w.blk;
+  s.c_first = xs / w.per_cta;
+  s.n_pieces = (xs + w.nb - 1) / w.per_cta - s.c_first + 1;
   w.x += len;
   w.blk += len;
   if (w.blk == w.nb && w.x < w.end) {
@@ -173,10 +178,10 @@ __device__ Segment walk_take(const PrefillArgs &a, Walk &w) {
 
 // Positions of one KV head's units of a row, over the lanes of a warp.
 template <int D>
-__device__ __forceinline__ long long row_positions(const PrefillArgs &a, int qn, int L, int lane) {
+__device__ __forceinline__ int row_positions(const PrefillArgs &a, int qn, int L, int lane) {
   constexpr int NT = Cfg<D>::NT;
   const int tiles = (qn + NT * a.TQ - 1) / (NT * a.TQ);
-  long long sum = 0;
+  int sum = 0;
   for (int it = lane; it < tiles; it += 32) {
     const int t0 = it * NT * a.TQ;
     sum += a.unit_cost + span_of<Cfg<D>::T>(a, L, qn, t0, min(t0 + NT * a.TQ, qn)).nb;
@@ -189,7 +194,7 @@ __device__ __forceinline__ long long row_positions(const PrefillArgs &a, int qn,
 // This CTA's range, from the rows' positions (`rows`, of one KV head each, in
 // shared memory); one warp.
 template <int D>
-__device__ Walk walk_start(const PrefillArgs &a, long long *rows, int lane) {
+__device__ Walk walk_start(const PrefillArgs &a, int *rows, int lane) {
   constexpr int NT = Cfg<D>::NT;
   Walk w;
   w.b = w.h = w.it = w.tiles = w.q0 = w.qn = w.L = w.blk = w.nb = 0;
@@ -197,26 +202,26 @@ __device__ Walk walk_start(const PrefillArgs &a, long long *rows, int lane) {
   w.per_cta = 1;
   const int chunk = (a.B + 31) / 32;
   const int lo = min(lane * chunk, a.B), hi = min(lo + chunk, a.B);
-  long long sum = 0;
+  int sum = 0;
   for (int i = lo; i < hi; ++i) sum += rows[i];
-  long long incl = sum;
+  int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  const long long total = __shfl_sync(0xffffffffu, incl, 31) * a.Hkv;
-  long long run = incl - sum;
+  const int total = __shfl_sync(0xffffffffu, incl, 31) * a.Hkv;
+  int run = incl - sum;
   for (int i = lo; i < hi; ++i) {
     run += rows[i];
     rows[i] = run;
   }
   __syncwarp();
   if (total == 0) return w;
-  w.per_cta = (total + gridDim.x - 1) / gridDim.x;
-  const long long x0 = (long long)blockIdx.x * w.per_cta;
+  w.per_cta = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int x0 = blockIdx.x * w.per_cta;
   if (x0 >= total) return w;
-  w.end = min(x0 + w.per_cta, total);
+  w.end = min(w.per_cta, total - x0) + x0;
   int b0 = 0, b1 = a.B - 1;  // first row whose positions end past x0
   while (b0 < b1) {
     const int mid = (b0 + b1) >> 1;
@@ -225,19 +230,19 @@ __device__ Walk walk_start(const PrefillArgs &a, long long *rows, int lane) {
   w.b = b0;
   row_of(a, w.b, w.q0, w.qn, w.L);
   w.tiles = (w.qn + NT * a.TQ - 1) / (NT * a.TQ);
-  const long long pre = w.b > 0 ? rows[w.b - 1] : 0, width = rows[w.b] - pre;
-  const long long off = x0 - pre * a.Hkv;
-  w.h = (int)(off / width);
-  const long long in_head = off - w.h * width;
+  const int pre = w.b > 0 ? rows[w.b - 1] : 0, width = rows[w.b] - pre;
+  const int off = x0 - pre * a.Hkv;
+  w.h = off / width;
+  const int in_head = off - w.h * width;
   // the group of tiles that holds position in_head: scan them 32 at a time
-  long long before = 0;
+  int before = 0;
   for (int i0 = 0;; i0 += 32) {
     const int it = i0 + lane, t0 = it * NT * a.TQ;
     const int c = it < w.tiles ? a.unit_cost + span_of<Cfg<D>::T>(a, w.L, w.qn, t0, min(t0 + NT * a.TQ, w.qn)).nb : 0;
-    long long upto = c;
+    int upto = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += v;
     }
     upto += before;
@@ -246,8 +251,8 @@ __device__ Walk walk_start(const PrefillArgs &a, long long *rows, int lane) {
       const int l = __ffs(past) - 1;
       w.it = i0 + l;
       w.nb = __shfl_sync(0xffffffffu, c, l) - a.unit_cost;
-      const long long start = __shfl_sync(0xffffffffu, upto - c, l);
-      const int pos = (int)(in_head - start);
+      const int start = __shfl_sync(0xffffffffu, upto - c, l);
+      const int pos = in_head - start;
       w.blk = pos > a.unit_cost ? pos - a.unit_cost : 0;
       w.x = x0 - pos + a.unit_cost + w.blk;
       break;
@@ -272,7 +277,7 @@ __device__ void producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *s
     prefetch_tmap(&tm.kv.k);
     prefetch_tmap(&tm.kv.v);
   }
-  Walk w = walk_start<D>(a, reinterpret_cast<long long *>(smem), lane);
+  Walk w = walk_start<D>(a, reinterpret_cast<int *>(smem), lane);
   fence_proxy_async_smem();  // the scan's accesses precede the ring's loads
   __syncwarp();
   const int bt = a.box_tokens;
@@ -408,12 +413,15 @@ __device__ __forceinline__ Steps steps_of(const PrefillArgs &a, const Span &span
 }
 
 // ---------------------------------------------------------------------------
-// Issuing thread.  Its instructions between two products are what the tensor
-// cores wait for, so one lane runs the whole role: no warp-wide votes, and
-// operand descriptors stepped by additions.
+// Issuing warp.  What it does between two products is what the tensor cores
+// wait for.  All lanes walk through the work together, on values that the
+// compiler can see to be the same in all of them, and one elected lane
+// issues: the operands of tcgen05.mma are then in uniform registers already.
+// (A lane alone in the role moved five operands there for every product, and
+// issued one in 65 cycles whatever its size.)
 // ---------------------------------------------------------------------------
 template <int D, bool kBf16>
-__device__ void issuer(const PrefillArgs &a, uint8_t *smem, uint32_t tmem) {
+__device__ void issuer(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int lane) {
   using C = Cfg<D>;
   constexpr int T = C::T, NT = C::NT;
   constexpr uint32_t kHi = smem_desc_hi(1024);
@@ -425,92 +433,105 @@ __device__ void issuer(const PrefillArgs &a, uint8_t *smem, uint32_t tmem) {
   const uint32_t q_lo = smem_desc_lo(sbase + C::kQOff, 16);
   int seg_n = 0;
   int slot = 0, phase = 0;    // next ring slot and its phase
-  int blk_n[2] = {0, 0};      // blocks whose scores buffer u has held
-  auto wait = [&](int bar, int n, int code) { return mbar_wait_bounded(bars + 8 * bar, n & 1, a.err, code); };
+  // blocks issued, by barrier: with two tiles those of each tile, with one
+  // tile the even and the odd ones
+  int s_n[2] = {0, 0}, p_n[2] = {0, 0};
+  int last = 0;  // the tile (or parity) whose scores were issued last
+  auto wait = [&](int bar, int n, int code) { return warp_wait_bounded(bars + 8 * bar, n & 1, a.err, code, lane); };
   auto advance = [&](int &sl, int &ph) {
     if (++sl == C::kSlots) {
       sl = 0;
       ph ^= 1;
     }
   };
-  // S(tile t, buffer u) = Q_t K^T with K in ring slot sl
-  auto scores = [&](int t, int u, int sl) {
+  // S = Q_t K^T with K in ring slot sl, once the scores before it in the
+  // buffer are in registers; i: the tile, or with one tile the block's parity
+  auto scores = [&](int t, int i, int sl) {
+    const int before = C::NS == 1 ? last : i;
+    if (s_n[before] > 0 && !wait(C::B_SFREE + before, s_n[before] - 1, kErrWaitFull)) return false;
+    tc_fence_after();
     const uint32_t q = q_lo + t * (C::kQBytes / 16), k = smem_desc_lo(sbase + sl * C::kSlotBytes, 16);
+    const uint32_t d = tmem + (C::NS == 1 ? 0 : i * T);
+    if (elect_one()) {
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
-      mma_ss<kHi>(tmem + u * T, q + (kk / 4) * (kTileRows * 8) + (kk % 4) * 2, k + (kk / 4) * (T * 8) + (kk % 4) * 2,
-                  idesc_qk, kk > 0);
-    mma_commit(bars + 8 * (C::B_SFULL + u));
-    ++blk_n[u];
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_ss<kHi>(d, q + (kk / 4) * (kTileRows * 8) + (kk % 4) * 2, k + (kk / 4) * (T * 8) + (kk % 4) * 2, idesc_qk, kk > 0);
+      mma_commit(bars + 8 * (C::B_SFULL + i));
+    }
+    __syncwarp();
+    ++s_n[i];
+    last = i;
+    return true;
   };
   // O_t += P V over the 16-key steps [k0, k1) of the block in ring slot sl
-  auto values = [&](int t, int u, int sl, int k0, int k1, bool first) {
-    const uint32_t v = smem_desc_lo(sbase + sl * C::kSlotBytes, T * 128), o = tmem + C::kOCol + t * D, p = tmem + u * T;
-    if (k0 == 0 && k1 == T / 16) {
+  auto values = [&](int t, int i, int sl, int k0, int k1, bool first) {
+    const uint32_t v = smem_desc_lo(sbase + sl * C::kSlotBytes, T * 128), o = tmem + C::kOCol + t * D;
+    const uint32_t p = tmem + C::kPCol + i * (T / 2);
+    if (!wait(C::B_PREADY + i, p_n[i], kErrWaitFull)) return false;
+    tc_fence_after();
+    if (elect_one()) {
+      if (k0 == 0 && k1 == T / 16) {
 #pragma unroll
-      for (int kk = 0; kk < T / 16; ++kk) mma_ts<kHi>(o, p + kk * 8, v + kk * 128, kIdescPV, kk > 0 || !first);
-    } else {
-      for (int kk = k0; kk < k1; ++kk) mma_ts<kHi>(o, p + kk * 8, v + kk * 128, kIdescPV, kk > k0 || !first);
+        for (int kk = 0; kk < T / 16; ++kk) mma_ts<kHi>(o, p + kk * 8, v + kk * 128, kIdescPV, kk > 0 || !first);
+      } else {
+        for (int kk = k0; kk < k1; ++kk) mma_ts<kHi>(o, p + kk * 8, v + kk * 128, kIdescPV, kk > k0 || !first);
+      }
+      mma_commit(bars + 8 * (C::B_OFULL + i));
     }
+    __syncwarp();
+    ++p_n[i];
+    return true;
   };
 
   for (;; ++seg_n) {
     const int d = seg_n % kDescs;
     if (!wait(C::B_DFULL + d, seg_n / kDescs, kErrWaitQ)) return;
-    const Segment s = descs[d];
-    mbar_arrive(bars + 8 * (C::B_DEMPTY + d));
+    Segment s;
+    s.kind = __shfl_sync(0xffffffffu, descs[d].kind, 0);
+    s.it = __shfl_sync(0xffffffffu, descs[d].it, 0);
+    s.qn = __shfl_sync(0xffffffffu, descs[d].qn, 0);
+    s.L = __shfl_sync(0xffffffffu, descs[d].L, 0);
+    s.beg = __shfl_sync(0xffffffffu, descs[d].beg, 0);
+    s.end = __shfl_sync(0xffffffffu, descs[d].end, 0);
+    if (lane == 0) mbar_arrive(bars + 8 * (C::B_DEMPTY + d));
     if (s.kind < 0) return;
     const int t0 = s.it * NT * a.TQ;
     const int tiles = min(NT, (s.qn - t0 + a.TQ - 1) / a.TQ);
     const Span span = span_of<T>(a, s.L, s.qn, t0, min(t0 + NT * a.TQ, s.qn));
     const int n = s.end - s.beg;
     if (!wait(C::B_QFULL, seg_n, kErrWaitQ)) return;
-    if (!wait(C::B_FULL + slot, phase, kErrWaitFull)) return;
-    if constexpr (NT == 2) {
-      for (int t = 0; t < tiles; ++t) scores(t, t, slot);
-    } else {
-      scores(0, (blk_n[0] + blk_n[1]) & 1, slot);
-    }
-    mma_commit(bars + 8 * (C::B_EMPTY + slot));
-    if (n == 1) mma_commit(bars + 8 * C::B_QEMPTY);
-    advance(slot, phase);
-    for (int j = 0; j < n; ++j) {
+    // Block j's scores are issued before the values of block j - 1, tile by
+    // tile: while a tile's softmax works on one block, its next scores wait
+    // in tensor memory and the tensor cores work for the other tile.
+    for (int j = -1; j < n; ++j) {
       const bool next = j + 1 < n;
-      const int vs = slot, v_phase = phase;
-      advance(slot, phase);
-      const int ks = slot, k_phase = phase;
-      const Steps st = steps_of<T>(a, span, span.block(s.beg + j) * T);
-      if (!wait(C::B_FULL + vs, v_phase, kErrWaitFull)) return;
-      if constexpr (NT == 2) {
-        for (int t = 0; t < tiles; ++t) {
-          if (!wait(C::B_PREADY + t, blk_n[t] - 1, kErrWaitFull)) return;
-          tc_fence_after();
-          values(t, t, vs, st.k0, st.k1, j == 0);
-          if (next) {
-            if (t == 0 && !wait(C::B_FULL + ks, k_phase, kErrWaitFull)) return;
-            scores(t, t, ks);
-          } else {
-            mma_commit(bars + 8 * (C::B_OFULL + t));
-          }
-        }
-      } else {
-        const int u = (blk_n[0] + blk_n[1] - 1) & 1, nu = blk_n[u] - 1;  // this block's buffer and its use
-        if (next) {
-          if (!wait(C::B_FULL + ks, k_phase, kErrWaitFull)) return;
-          scores(0, u ^ 1, ks);
-          mma_commit(bars + 8 * (C::B_EMPTY + ks));
-        }
-        if (!wait(C::B_PREADY + u, nu, kErrWaitFull)) return;
-        tc_fence_after();
-        values(0, u, vs, st.k0, st.k1, j == 0);
-        mma_commit(bars + 8 * C::B_OFULL);
-      }
-      mma_commit(bars + 8 * (C::B_EMPTY + vs));
-      if (next) {
-        if (NT == 2) mma_commit(bars + 8 * (C::B_EMPTY + ks));
-        if (j + 2 == n) mma_commit(bars + 8 * C::B_QEMPTY);
+      int vs = 0, v_phase = 0;
+      if (j >= 0) {
+        vs = slot;
+        v_phase = phase;
         advance(slot, phase);
       }
+      const int ks = slot;
+      Steps st;
+      if (j >= 0) st = steps_of<T>(a, span, span.block(s.beg + j) * T);
+      if (next && !wait(C::B_FULL + ks, phase, kErrWaitFull)) return;
+      for (int t = 0; t < tiles; ++t) {
+        if (next) {
+          if (!scores(t, NT == 2 ? t : (s_n[0] + s_n[1]) & 1, ks)) return;
+          if (t + 1 == tiles && elect_one()) {
+            mma_commit(bars + 8 * (C::B_EMPTY + ks));
+            if (j + 2 == n) mma_commit(bars + 8 * C::B_QEMPTY);
+          }
+          __syncwarp();
+        }
+        if (j >= 0) {
+          if (t == 0 && !wait(C::B_FULL + vs, v_phase, kErrWaitFull)) return;
+          if (!values(t, NT == 2 ? t : (p_n[0] + p_n[1]) & 1, vs, st.k0, st.k1, j == 0)) return;
+        }
+      }
+      if (j >= 0 && elect_one()) mma_commit(bars + 8 * (C::B_EMPTY + vs));
+      __syncwarp();
+      if (next) advance(slot, phase);
     }
   }
 }
@@ -518,6 +539,53 @@ __device__ void issuer(const PrefillArgs &a, uint8_t *smem, uint32_t tmem) {
 // n ones from bit 0 up, for any n.
 __device__ __forceinline__ uint32_t bits_below(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// Maximum of a row's scores, but for the groups of 32 in `none` (kEdge only;
+// a block away from every edge is straight-line code).
+template <int T, bool kEdge>
+__device__ __forceinline__ float row_max(const float (&x)[T], uint32_t none) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int c = 0; c < T; c += 32) {
+    if (kEdge && ((none >> (c / 32)) & 1u)) continue;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], x[c + i], x[c + i + 1]);
+  }
+  return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+}
+
+// Of kPolyOf pairs of weights, kPoly are computed on the floating-point pipe.
+constexpr int kPoly = 0, kPolyOf = 4;
+
+// The row's weights 2^(scale x + base), rounded to the input type, two in a
+// word; returns their sum (before the rounding).
+template <int T, bool kBf16, bool kEdge>
+__device__ __forceinline__ float weights(const float (&x)[T], uint32_t none, float scale, float base, uint32_t (&p)[T / 2]) {
+  const float2 sc = make_float2(scale, scale), bs = make_float2(base, base);
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int c = 0; c < T; c += 32) {
+    if (kEdge && ((none >> (c / 32)) & 1u)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) p[c / 2 + i] = 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        float2 e = fma2(make_float2(x[c + i], x[c + i + 1]), sc, bs);
+        if (!kEdge && (i >> 1) % kPolyOf < kPoly) {
+          e = ex2_poly(e);
+        } else {
+          e.x = ex2(e.x);
+          e.y = ex2(e.y);
+        }
+        sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
+        p[(c + i) / 2] = pack2<kBf16>(e.x, e.y);
+      }
+    }
+  }
+  sum[0] = add2(sum[0], sum[1]);
+  return sum[0].x + sum[0].y;
 }
 
 // ---------------------------------------------------------------------------
@@ -536,7 +604,6 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
   // becomes one that leaves nothing of a score, since -inf marks a masked one.
   const float sl2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
   int seg_n = 0, blk_n = 0;   // segments and score blocks seen
-  int o_n = 0;                // uses of this tile's accumulator barrier (below)
   int slot_n = 1;             // ring slot, of all so far, that holds the current block's values
   auto wait = [&](int bar, int n, int code) { return warp_wait_bounded(bars + 8 * bar, n & 1, a.err, code, lane); };
 
@@ -560,35 +627,46 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     int lim = a.causal ? min(s.L, s.L - s.qn + tok + 1) : s.L;
     if (!real) lim = 0;
     const int low = a.window > 0 ? max(lim - a.window, 0) : 0;
-    // a block needs the mask unless every row of the tile sees all of it
+    // a block lies at an edge unless every row of the tile sees all of it;
+    // one whose values need clearing always does: its hidden keys lie past
+    // every row's, or before every row's window
     const int tile_lim = a.causal ? s.L - s.qn + tt0 + 1 : s.L;
     const int tile_low = a.window > 0 ? s.L - s.qn + min(tt0 + a.TQ, s.qn) - a.window : 0;
 
     float m = -INFINITY, l = 0.f;  // running maximum (base 2, scaled) and sum
     for (int blk = s.beg; blk < s.end; ++blk) {
+      // barriers: the tile's, or with one tile those of the block's parity
       const int u = NT == 2 ? t : blk_n & 1, un = NT == 2 ? blk_n : blk_n >> 1;
       if (!wait(C::B_SFULL + u, un, kErrWaitFull)) return;
       tc_fence_after();
       ++blk_n;
-      const uint32_t s_addr = tmem + lanes + u * T;
+      const uint32_t s_addr = tmem + lanes + (C::NS == 1 ? 0 : u * T);
       float x[T];
 #pragma unroll
       for (int c = 0; c < T; c += 32) tmem_ld32(s_addr + c, reinterpret_cast<uint32_t *>(x + c));
       tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (C::B_SFREE + u));
       const int j0 = span.block(blk) * T;
-      if (j0 + T > tile_lim || (j0 < tile_low && j0 + T > a.sinks)) {
+      // The keys that this warp's rows see, 32 at a time: all, none or some.
+      // Only a block at an edge of the masks looks.
+      const bool edge = j0 + T > tile_lim || (j0 < tile_low && j0 + T > a.sinks);
+      uint32_t none = 0;  // bit c: keys 32 c .. 32 c + 31 are hidden from all rows of the warp
+      if (edge) {
 #pragma unroll
-        for (int c = 0; c < T; c += 32) {  // one bit a key: seen or not
+        for (int c = 0; c < T; c += 32) {
           const int j = j0 + c;
           const uint32_t seen = bits_below(lim - j) & (~bits_below(low - j) | bits_below(a.sinks - j));
+          if (!__any_sync(0xffffffffu, seen != 0)) {
+            none |= 1u << (c / 32);
+          } else if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[c + i] = (seen >> i) & 1u ? x[c + i] : -INFINITY;
+            for (int i = 0; i < 32; ++i) x[c + i] = (seen >> i) & 1u ? x[c + i] : -INFINITY;
+          }
         }
       }
-      float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-      for (int i = 4; i < T; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+      const float top = (edge ? row_max<T, true>(x, none) : row_max<T, false>(x, 0)) * sl2;
       // The reference m follows the maximum only once it is 2^8 behind, so
       // the accumulator is hardly ever rescaled; weights stay below 2^8.
       const bool behind = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
@@ -598,9 +676,9 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
         m = mn;
         l *= alpha;
         if (blk > s.beg) {
-          // These scores were issued after the values of the block before
-          // (two tiles), or are waited for apart from them (one tile).
-          if (NT == 1 && !wait(C::B_OFULL, o_n - 1, kErrWaitFull)) return;
+          // the values of the block before are in the accumulator
+          const int pu = NT == 2 ? t : u ^ 1, pn = NT == 2 ? un - 1 : (blk_n - 2) >> 1;
+          if (!wait(C::B_OFULL + pu, pn, kErrWaitFull)) return;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
@@ -613,81 +691,90 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
           }
         }
       }
-      const float base = m == -INFINITY ? 0.f : -m;
-      const float2 sc = make_float2(sl2, sl2), bs = make_float2(base, base);
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int c = 0; c < T; c += 32) {
-        uint32_t p[16];
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          float2 e = fma2(make_float2(x[c + i], x[c + i + 1]), sc, bs);
-          e.x = ex2(e.x);
-          e.y = ex2(e.y);
-          sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
-          p[i >> 1] = pack2<kBf16>(e.x, e.y);
-        }
-        tmem_st16(s_addr + (c >> 1), p);
-      }
-      sum[0] = add2(sum[0], sum[1]);
-      l += sum[0].x + sum[0].y;
       if (t == 0) {
-        const Steps st = steps_of<T>(a, span, j0);
-        if (st.clear) {  // the row's last block, or one at the window's start: values of hidden keys become zeros
-          const int sl = slot_n % C::kSlots;
-          if (!wait(C::B_FULL + sl, slot_n / C::kSlots, kErrWaitFull)) return;
-          const uint32_t v = sbase + sl * C::kSlotBytes;
-          for (int i = st.k0 * 16 * (D / 8) + r; i < st.k1 * 16 * (D / 8); i += kTileRows) {
-            const int key = i / (D / 8), c = i % (D / 8);
-            if (key >= st.top || (key >= st.g0 && key < st.g1))
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + (c / 8) * (T * 128) + key * 128 + (c % 8) * 16),
-                           "r"(0u) : "memory");
+        if (edge) {
+          const Steps st = steps_of<T>(a, span, j0);
+          if (st.clear) {  // values of hidden keys become zeros
+            const int sl = slot_n % C::kSlots;
+            if (!wait(C::B_FULL + sl, slot_n / C::kSlots, kErrWaitFull)) return;
+            const uint32_t v = sbase + sl * C::kSlotBytes;
+            for (int i = st.k0 * 16 * (D / 8) + r; i < st.k1 * 16 * (D / 8); i += kTileRows) {
+              const int key = i / (D / 8), c = i % (D / 8);
+              if (key >= st.top || (key >= st.g0 && key < st.g1))
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + (c / 8) * (T * 128) + key * 128 + (c % 8) * 16),
+                             "r"(0u) : "memory");
+            }
+            fence_proxy_async_smem();  // before the product reads them
+            __syncwarp();
           }
-          fence_proxy_async_smem();  // before the product reads them
-          __syncwarp();
         }
         slot_n += 2;
       }
+      const float base = m == -INFINITY ? 0.f : -m;
+      uint32_t p[T / 2];
+      l += edge ? weights<T, kBf16, true>(x, none, sl2, base, p) : weights<T, kBf16, false>(x, 0, sl2, base, p);
+      // the product that read the buffer's weights before is done
+      if (un > 0 && !wait(C::B_OFULL + u, un - 1, kErrWaitFull)) return;
+      tc_fence_after();
+      const uint32_t p_addr = tmem + lanes + C::kPCol + u * (T / 2);
+#pragma unroll
+      for (int c = 0; c < T / 2; c += 16) tmem_st16(p_addr + c, p + c);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(bars + 8 * (C::B_PREADY + u));
-      if (NT == 1) ++o_n;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (C::B_PREADY + u));
     }
 
     // ---- the rows: O / l and LSE ----
-    // With one tile the last scores were issued before the values of the
-    // block before, which may not be done: its phase is waited for first
-    // (a parity tells neighbouring phases apart, not the one before).
-    if (NT == 1 && o_n > 1 && !wait(C::B_OFULL, o_n - 2, kErrWaitFull)) return;
-    if (NT == 2) ++o_n;  // once a unit; with one tile, once a block
-    if (!wait(C::B_OFULL + t, o_n - 1, kErrWaitFull)) return;
+    const int lu = NT == 2 ? t : (blk_n - 1) & 1;  // the last block's values
+    if (!wait(C::B_OFULL + lu, NT == 2 ? blk_n - 1 : (blk_n - 1) >> 1, kErrWaitFull)) return;
     tc_fence_after();
     const float inv = 1.f / l;
     const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     const int hq = s.h * a.G + r % a.G;
-    const size_t piece = s.kind == 0 ? 0 : (size_t)blockIdx.x * 2 + (s.kind - 1);
-    const size_t piece_row = piece * (NT * kTileRows) + t * kTileRows + r;
+    // Where the row goes: row `row` of the output, or of the CTA's piece slot.
+    const int out_row = (s.q0 + tok) * a.Hq + hq;
+    const int piece_row = (blockIdx.x * 2 + (s.kind - 1)) * (NT * kTileRows) + t * kTileRows + r;
+    const int row = !real ? -1 : s.kind == 0 ? out_row : piece_row;
+    uint8_t *stage = smem + C::kStageOff + (t * 4 + warp) * 4096;
+    uint8_t *dst = s.kind == 0 ? static_cast<uint8_t *>(a.out) : reinterpret_cast<uint8_t *>(a.o_part);
+    const int pitch = s.kind == 0 ? D * 2 : D * 4;  // bytes of a row
+    // 128 bytes of every row at a time, through shared memory (16-byte chunks
+    // swizzled by the row), so that 8 lanes write a row's bytes together: a
+    // lane writing its own row would touch 32 lines with every store.
+    auto flush = [&](int at) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int rr = i * 4 + (lane >> 3), c = lane & 7;
+        const int to = __shfl_sync(0xffffffffu, row, rr);
+        const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
+        if (to >= 0) *reinterpret_cast<uint4 *>(dst + (size_t)to * pitch + at + c * 16) = v;
+      }
+      __syncwarp();
+    };
+    auto put = [&](int c, uint4 v) { *reinterpret_cast<uint4 *>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = v; };
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       float o[32];
       tmem_ld32(o_addr + c, reinterpret_cast<uint32_t *>(o));
       tmem_wait_ld();
-      if (real) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;  // no key: O holds nothing to read
-        if (s.kind == 0) {
-          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + ((size_t)(s.q0 + tok) * a.Hq + hq) * D + c);
+      for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;  // no key: O holds nothing to read
+      if (s.kind == 0) {
+        const int half = (c >> 5) & 1;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[i] = make_uint4(pack2<kBf16>(o[8 * i], o[8 * i + 1]), pack2<kBf16>(o[8 * i + 2], o[8 * i + 3]),
-                                pack2<kBf16>(o[8 * i + 4], o[8 * i + 5]), pack2<kBf16>(o[8 * i + 6], o[8 * i + 7]));
-        } else {
-          float4 *dst = reinterpret_cast<float4 *>(a.o_part + piece_row * D + c);
+        for (int i = 0; i < 4; ++i)
+          put(half * 4 + i, make_uint4(pack2<kBf16>(o[8 * i], o[8 * i + 1]), pack2<kBf16>(o[8 * i + 2], o[8 * i + 3]),
+                                       pack2<kBf16>(o[8 * i + 4], o[8 * i + 5]), pack2<kBf16>(o[8 * i + 6], o[8 * i + 7])));
+        if (half) flush((c - 32) * 2);
+      } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        }
+        for (int i = 0; i < 8; ++i)
+          put(i, make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
+                            __float_as_uint(o[4 * i + 3])));
+        flush(c * 4);
       }
-      __syncwarp();
     }
     if (real) {
       if (s.kind == 0) {
@@ -729,7 +816,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars + 8 * (C::B_SFULL + i), 1);
-      mbar_init(bars + 8 * (C::B_PREADY + i), kTileRows);
+      mbar_init(bars + 8 * (C::B_SFREE + i), 4);  // one arrival a softmax warp
+      mbar_init(bars + 8 * (C::B_PREADY + i), 4);
       mbar_init(bars + 8 * (C::B_OFULL + i), 1);
     }
     mbar_init(bars + 8 * C::B_QFULL, 1);
@@ -746,11 +834,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   // this launch depends on.
   grid_dependency_wait();
   // the rows' positions, for the producer's scan (the ring is still unused)
-  long long *rows = reinterpret_cast<long long *>(smem);
+  int *rows = reinterpret_cast<int *>(smem);
   for (int b = warp; b < a.B; b += C::kThreads / 32) {
     int q0, qn, L;
     row_of(a, b, q0, qn, L);
-    const long long n = row_positions<D>(a, qn, L, lane);
+    const int n = row_positions<D>(a, qn, L, lane);
     if (lane == 0) {
       rows[b] = n;
       if (b % (int)gridDim.x == (int)blockIdx.x) check_row(a, b);
@@ -763,12 +851,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   tc_fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
+  tmem = __shfl_sync(0xffffffffu, tmem, 0);
   if (warp >= C::kSoftmaxWarps) {
     if constexpr (C::NT == 2) regs_dec<88>();  // 168 a thread at launch: 384 x 168 = 256 x 208 + 128 x 88
-    if (warp == C::kMmaWarp) {
-      if (lane == 0) issuer<D, kBf16>(a, smem, tmem);
-      __syncwarp();
-    } else if (warp == C::kProducerWarp) producer<D, kBf16>(tm, a, smem, lane);
+    if (warp == C::kMmaWarp) issuer<D, kBf16>(a, smem, tmem, lane);
+    else if (warp == C::kProducerWarp) producer<D, kBf16>(tm, a, smem, lane);
     else if (warp == C::kQueryWarp) queries<D>(tm, a, smem, lane);
   } else {
     if constexpr (C::NT == 2) regs_inc<208>();
@@ -783,11 +870,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 // ---------------------------------------------------------------------------
 // Merge of the units that ranges cut: cut i (between CTAs i - 1 and i) of a
 // unit with n pieces takes the (i - c_first)-th share of its rows, and
-// blockIdx.y a part of that.  LSE = ln sum exp(lse_p), O = sum exp(lse_p - LSE) O_p.
+// blockIdx.y a part of that: two rows a warp where a unit has two pieces, since
+// a row is a chain of a few dependent loads.  LSE = ln sum exp(lse_p), O = sum exp(lse_p - LSE) O_p.
 // One warp a row.
 // ---------------------------------------------------------------------------
+constexpr int kMergeThreads = 256, kMergeParts = 16;
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ PrefillArgs a) {
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ PrefillArgs a) {
   constexpr int NT = Cfg<D>::NT;
   constexpr float kLog2e = 1.4426950408889634f;
   grid_launch_dependents();
@@ -798,8 +887,9 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Pref
   if (n < 2) return;
   const int lane = threadIdx.x & 31;
   const int rows = pd.tokens * a.G;
-  const int parts = (n - 1) * gridDim.y * 4;
-  const int part = ((cta - pd.c_first - 1) * gridDim.y + blockIdx.y) * 4 + (threadIdx.x >> 5);
+  constexpr int kWarps = kMergeThreads / 32;
+  const int parts = (n - 1) * gridDim.y * kWarps;
+  const int part = ((cta - pd.c_first - 1) * gridDim.y + blockIdx.y) * kWarps + (threadIdx.x >> 5);
   const int beg = (int)((long long)rows * part / parts), end = (int)((long long)rows * (part + 1) / parts);
   auto slot_of = [&](int i) -> size_t { return i == 0 ? (size_t)pd.c_first * 2 + 1 : (size_t)(pd.c_first + i) * 2; };
   for (int m = beg; m < end; ++m) {
@@ -888,8 +978,8 @@ mxa_status_t launch_typed(const PrefillLaunch &L, PrefillArgs a, cudaStream_t st
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, prefill_kernel<D, kBf16>, tm, a) != cudaSuccess) return MXA_ERR_CUDA;
   if (L.plan.grid > 1) {
-    cfg.gridDim = dim3((unsigned)(L.plan.grid - 1), 4);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)(L.plan.grid - 1), kMergeParts);
+    cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, merge_kernel<D, kBf16>, a) != cudaSuccess) return MXA_ERR_CUDA;
   }
@@ -935,15 +1025,29 @@ mxa_status_t launch_prefill(const PrefillLaunch &L, cudaStream_t stream) {
   return bf16 ? launch_typed<256, true>(L, a, stream) : launch_typed<256, false>(L, a, stream);
 }
 
+namespace {
+constexpr int kUnitCost = 1;
+// Upper bound on the units of one KV head: every row's last group of tiles may be partial.
+long long max_groups(const mxa_decode_params_t &p, int total_q) {
+  const int G = p.Hq / p.Hkv, tokens = (p.D <= 128 ? 2 : 1) * (kTileRows / G);
+  return (long long)total_q / tokens + (p.B < total_q ? p.B : total_q);
+}
+long long max_blocks(const mxa_decode_params_t &p) {
+  const int T = p.D <= 128 ? 128 : 64;
+  return ((long long)p.max_seqlen_k + T - 1) / T + 1;
+}
+}  // namespace
+
+long long prefill_positions(const mxa_decode_params_t &p, int total_q) {
+  return max_groups(p, total_q) * p.Hkv * (max_blocks(p) + kUnitCost);
+}
+
 // One CTA per SM, and no more than the work can feed with two blocks each.
 PrefillPlan plan_prefill(const mxa_decode_params_t &p, int total_q, int sm_count) {
-  const int G = p.Hq / p.Hkv, NT = p.D <= 128 ? 2 : 1, T = p.D <= 128 ? 128 : 64, TQ = kTileRows / G;
+  const int NT = p.D <= 128 ? 2 : 1;
   PrefillPlan plan = {};
-  plan.unit_cost = 1;
-  // every row's last group may be partial
-  const long long groups = (long long)total_q / (NT * TQ) + (p.B < total_q ? p.B : total_q);
-  const long long blocks = ((long long)p.max_seqlen_k + T - 1) / T + 1;
-  const long long cap = groups * p.Hkv * ((blocks + 1) / 2);
+  plan.unit_cost = kUnitCost;
+  const long long cap = max_groups(p, total_q) * p.Hkv * ((max_blocks(p) + 1) / 2);
   plan.grid = (int)(cap < sm_count ? (cap < 1 ? 1 : cap) : sm_count);
   plan.lse_off = align256(sizeof(PieceDesc) * (size_t)plan.grid);
   const size_t rows = plan.grid > 1 ? (size_t)plan.grid * 2 * NT * kTileRows : 0;

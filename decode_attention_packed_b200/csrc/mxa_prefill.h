@@ -44,6 +44,8 @@ struct PrefillPlan {
   int grid, unit_cost;
   size_t lse_off, o_off, workspace_bytes;
 };
+// Upper bound on the positions that the work of a call is laid out on.
+long long prefill_positions(const mxa_decode_params_t &p, int total_q);
 PrefillPlan plan_prefill(const mxa_decode_params_t &p, int total_q, int sm_count);
 
 struct PrefillLaunch {

@@ -109,6 +109,13 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // ---- packed float32 arithmetic: two lanes of a 64-bit register pair ----
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -124,6 +131,42 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// 2^x on the floating-point pipe, for x < 100, to relieve the special-function
+// unit: x = n + f with n the nearest integer (added to and taken from 1.5 *
+// 2^23, where a float's last bit is one: Cody and Waite's reduction), 2^f by a
+// polynomial of degree 4 (least maximal relative error over [-1/2, 1/2],
+// fitted by Lawson's algorithm: 2.7e-6), times 2^n, whose exponent bits are
+// the sum's last ones.  x below -126 gives 2^-126 instead of less; NaN stays.
+__device__ __forceinline__ float2 ex2_poly(float2 x) {
+  constexpr float kShift = 12582912.f + 127.f;
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-126.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-126.f));
+  const float2 t = add2(x, make_float2(kShift, kShift));
+  const float2 n = add2(t, make_float2(-kShift, -kShift));
+  const float2 f = fma2(n, make_float2(-1.f, -1.f), x);
+  auto c = [](float v) { return make_float2(v, v); };
+  float2 p = fma2(c(0.009570102207362652f), f, c(0.05591785907745361f));
+  p = fma2(p, f, c(0.240247443318367f));
+  p = fma2(p, f, c(0.6931217908859253f));
+  p = fma2(p, f, c(0.9999992847442627f));
+  return mul2(p, make_float2(__uint_as_float(__float_as_uint(t.x) << 23), __uint_as_float(__float_as_uint(t.y) << 23)));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
