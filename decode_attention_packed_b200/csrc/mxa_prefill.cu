@@ -7,10 +7,10 @@
 //  - a producer warp finds the CTA's share, gathers K and V pages through the
 //    block table with TMA into a ring of shared-memory slots; a query warp
 //    loads the packed query rows;
-//  - an issuing warp runs S = Q K^T and O += P V on the tensor cores
+//  - two issuing warps run S = Q K^T and O += P V on the tensor cores
 //    (tcgen05, accumulators and P in tensor memory);
-//  - one or two softmax warpgroups, one thread per packed query row, turn S
-//    into P with a running maximum and sum, and write the rows out.
+//  - softmax warps, two threads per packed query row, turn S into P with a
+//    running maximum and sum, and write the rows out.
 //
 // Units.  The G query heads of one KV head are packed into the rows of a
 // tile, row m = t * G + g, so a KV byte serves all of them: a 128-row tile
@@ -25,8 +25,6 @@
 // batches, causal triangles and single long rows all give every CTA the same
 // work.  A unit cut by a range's end leaves float32 pieces with their LSEs in
 // the workspace, which a second small kernel merges.
-#include <type_traits>
-
 #include "mxa_config.h"
 #include "mxa_device.cuh"
 #include "mxa_launch.h"
@@ -46,11 +44,12 @@ struct Cfg {
   static constexpr int NT = D <= 128 ? 2 : 1;       // tiles of a unit
   static constexpr int T = D <= 128 ? 128 : 64;     // keys of a block
   static constexpr int CH = D / 64;                 // 64-column chunks of a row
-  static constexpr int kSoftmaxWarps = 4 * NT;
-  static constexpr int kMmaWarp = kSoftmaxWarps, kProducerWarp = kSoftmaxWarps + 1, kQueryWarp = kSoftmaxWarps + 2;
-  static constexpr int kThreads = 128 * (NT + 1);
+  static constexpr int kSoftmaxWarps = 8 * NT;      // two threads a row
+  static constexpr int kScoreWarp = kSoftmaxWarps, kValueWarp = kSoftmaxWarps + 1;
+  static constexpr int kProducerWarp = kSoftmaxWarps + 2, kQueryWarp = kSoftmaxWarps + 3;
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
   static constexpr int kSlotBytes = T * D * 2;      // one block of K or of V
-  static constexpr int kSlots = 128 * 1024 / kSlotBytes;
+  static constexpr int kSlots = 128 * 1024 / kSlotBytes;  // even: keys in the even slots, values in the odd ones
   static constexpr int kQBytes = kTileRows * D * 2;
   // Tensor memory: NS score buffers of T columns, two weight buffers of T / 2
   // (a column holds two weights of a row), then the tiles' accumulators.  At
@@ -61,15 +60,18 @@ struct Cfg {
   static_assert(kPCol + T <= kOCol, "tensor memory");
   // shared memory
   static constexpr int kQOff = kSlots * kSlotBytes;
-  static constexpr int kStageOff = kQOff + NT * kQBytes;  // 4 KB a softmax warp, for the rows it writes out
-  static constexpr int kDescOff = kStageOff + kSoftmaxWarps * 4096;
+  // 2 KB a softmax warp: maxima and sums for the other half of its rows, and
+  // the rows it writes out
+  static constexpr int kStageOff = kQOff + NT * kQBytes;
+  static constexpr int kDescOff = kStageOff + kSoftmaxWarps * 2048;
   static constexpr int kBarOff = kDescOff + kDescs * 64;
   static constexpr int kSmem = kBarOff + 512;
   // barriers
   static constexpr int B_FULL = 0, B_EMPTY = kSlots, B_SFULL = 2 * kSlots, B_SFREE = B_SFULL + 2;
   static constexpr int B_PREADY = B_SFREE + 2;
   static constexpr int B_OFULL = B_PREADY + 2, B_QFULL = B_OFULL + 2, B_QEMPTY = B_QFULL + 1;
-  static constexpr int B_DFULL = B_QEMPTY + 1, B_DEMPTY = B_DFULL + kDescs, B_COUNT = B_DEMPTY + kDescs;
+  static constexpr int B_DFULL = B_QEMPTY + 1, B_DEMPTY = B_DFULL + kDescs, B_XCHG = B_DEMPTY + kDescs;
+  static constexpr int B_COUNT = B_XCHG + 4 * NT;
   static_assert(B_COUNT * 8 + 16 <= 512 && kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -413,125 +415,135 @@ __device__ __forceinline__ Steps steps_of(const PrefillArgs &a, const Span &span
 }
 
 // ---------------------------------------------------------------------------
-// Issuing warp.  What it does between two products is what the tensor cores
-// wait for.  All lanes walk through the work together, on values that the
-// compiler can see to be the same in all of them, and one elected lane
-// issues: the operands of tcgen05.mma are then in uniform registers already.
-// (A lane alone in the role moved five operands there for every product, and
-// issued one in 65 cycles whatever its size.)
+// Issuing warps: one for the scores and one for the values, so that one's
+// waits and bookkeeping pass while the other's products run (a single warp
+// spent as long on them as the tensor cores on its products).  All lanes of a
+// warp walk through the work together, on values that the compiler can see
+// to be the same in all of them, and one elected lane issues: the operands of
+// tcgen05.mma are then in uniform registers already (a lane alone in the role
+// moved five operands there for every product, and issued one in 65 cycles
+// whatever its size).
 // ---------------------------------------------------------------------------
+
+// The next segment, for a whole warp; kind < 0: none.
+struct Work {
+  int kind, n, tiles, beg;
+  Span span;
+};
+template <int D>
+__device__ __forceinline__ bool take_segment(const PrefillArgs &a, uint8_t *smem, int seg_n, int lane, Work &w) {
+  using C = Cfg<D>;
+  const uint32_t bars = smem_addr(smem) + C::kBarOff;
+  const int d = seg_n % kDescs;
+  if (!warp_wait_bounded(bars + 8 * (C::B_DFULL + d), (seg_n / kDescs) & 1, a.err, kErrWaitQ, lane)) return false;
+  const Segment *s = reinterpret_cast<const Segment *>(smem + C::kDescOff) + d;
+  w.kind = __shfl_sync(0xffffffffu, s->kind, 0);
+  const int it = __shfl_sync(0xffffffffu, s->it, 0), qn = __shfl_sync(0xffffffffu, s->qn, 0);
+  const int L = __shfl_sync(0xffffffffu, s->L, 0);
+  w.beg = __shfl_sync(0xffffffffu, s->beg, 0);
+  w.n = __shfl_sync(0xffffffffu, s->end, 0) - w.beg;
+  if (lane == 0) mbar_arrive(bars + 8 * (C::B_DEMPTY + d));
+  const int t0 = it * C::NT * a.TQ;
+  w.tiles = min(C::NT, (qn - t0 + a.TQ - 1) / a.TQ);
+  w.span = span_of<C::T>(a, L, qn, t0, min(t0 + C::NT * a.TQ, qn));
+  return true;
+}
+
+// S = Q_t K^T of every block and tile, once the scores before them in the
+// buffer are in registers: a tile's next scores wait in tensor memory while
+// its softmax works on a block.
 template <int D, bool kBf16>
-__device__ void issuer(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int lane) {
+__device__ void issue_scores(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int lane) {
   using C = Cfg<D>;
   constexpr int T = C::T, NT = C::NT;
   constexpr uint32_t kHi = smem_desc_hi(1024);
-  constexpr uint32_t kIdescPV = mma_idesc<kBf16>(kTileRows, D, true);
   // a negative scale becomes positive with Q negated
-  const uint32_t idesc_qk = mma_idesc<kBf16>(kTileRows, T, false) | (a.scale_log2 < 0.f ? kIdescNegateA : 0u);
+  const uint32_t idesc = mma_idesc<kBf16>(kTileRows, T, false) | (a.scale_log2 < 0.f ? kIdescNegateA : 0u);
   const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
-  const Segment *descs = reinterpret_cast<const Segment *>(smem + C::kDescOff);
   const uint32_t q_lo = smem_desc_lo(sbase + C::kQOff, 16);
-  int seg_n = 0;
-  int slot = 0, phase = 0;    // next ring slot and its phase
+  int slot = 0, phase = 0;  // ring slot of the next keys, and its phase
   // blocks issued, by barrier: with two tiles those of each tile, with one
   // tile the even and the odd ones
-  int s_n[2] = {0, 0}, p_n[2] = {0, 0};
+  int s_n[2] = {0, 0};
   int last = 0;  // the tile (or parity) whose scores were issued last
   auto wait = [&](int bar, int n, int code) { return warp_wait_bounded(bars + 8 * bar, n & 1, a.err, code, lane); };
-  auto advance = [&](int &sl, int &ph) {
-    if (++sl == C::kSlots) {
-      sl = 0;
-      ph ^= 1;
-    }
-  };
-  // S = Q_t K^T with K in ring slot sl, once the scores before it in the
-  // buffer are in registers; i: the tile, or with one tile the block's parity
-  auto scores = [&](int t, int i, int sl) {
-    const int before = C::NS == 1 ? last : i;
-    if (s_n[before] > 0 && !wait(C::B_SFREE + before, s_n[before] - 1, kErrWaitFull)) return false;
-    tc_fence_after();
-    const uint32_t q = q_lo + t * (C::kQBytes / 16), k = smem_desc_lo(sbase + sl * C::kSlotBytes, 16);
-    const uint32_t d = tmem + (C::NS == 1 ? 0 : i * T);
-    if (elect_one()) {
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma_ss<kHi>(d, q + (kk / 4) * (kTileRows * 8) + (kk % 4) * 2, k + (kk / 4) * (T * 8) + (kk % 4) * 2, idesc_qk, kk > 0);
-      mma_commit(bars + 8 * (C::B_SFULL + i));
-    }
-    __syncwarp();
-    ++s_n[i];
-    last = i;
-    return true;
-  };
-  // O_t += P V over the 16-key steps [k0, k1) of the block in ring slot sl
-  auto values = [&](int t, int i, int sl, int k0, int k1, bool first) {
-    const uint32_t v = smem_desc_lo(sbase + sl * C::kSlotBytes, T * 128), o = tmem + C::kOCol + t * D;
-    const uint32_t p = tmem + C::kPCol + i * (T / 2);
-    if (!wait(C::B_PREADY + i, p_n[i], kErrWaitFull)) return false;
-    tc_fence_after();
-    if (elect_one()) {
-      if (k0 == 0 && k1 == T / 16) {
-#pragma unroll
-        for (int kk = 0; kk < T / 16; ++kk) mma_ts<kHi>(o, p + kk * 8, v + kk * 128, kIdescPV, kk > 0 || !first);
-      } else {
-        for (int kk = k0; kk < k1; ++kk) mma_ts<kHi>(o, p + kk * 8, v + kk * 128, kIdescPV, kk > k0 || !first);
-      }
-      mma_commit(bars + 8 * (C::B_OFULL + i));
-    }
-    __syncwarp();
-    ++p_n[i];
-    return true;
-  };
-
-  for (;; ++seg_n) {
-    const int d = seg_n % kDescs;
-    if (!wait(C::B_DFULL + d, seg_n / kDescs, kErrWaitQ)) return;
-    Segment s;
-    s.kind = __shfl_sync(0xffffffffu, descs[d].kind, 0);
-    s.it = __shfl_sync(0xffffffffu, descs[d].it, 0);
-    s.qn = __shfl_sync(0xffffffffu, descs[d].qn, 0);
-    s.L = __shfl_sync(0xffffffffu, descs[d].L, 0);
-    s.beg = __shfl_sync(0xffffffffu, descs[d].beg, 0);
-    s.end = __shfl_sync(0xffffffffu, descs[d].end, 0);
-    if (lane == 0) mbar_arrive(bars + 8 * (C::B_DEMPTY + d));
-    if (s.kind < 0) return;
-    const int t0 = s.it * NT * a.TQ;
-    const int tiles = min(NT, (s.qn - t0 + a.TQ - 1) / a.TQ);
-    const Span span = span_of<T>(a, s.L, s.qn, t0, min(t0 + NT * a.TQ, s.qn));
-    const int n = s.end - s.beg;
+  Work w;
+  for (int seg_n = 0;; ++seg_n) {
+    if (!take_segment<D>(a, smem, seg_n, lane, w) || w.kind < 0) return;
     if (!wait(C::B_QFULL, seg_n, kErrWaitQ)) return;
-    // Block j's scores are issued before the values of block j - 1, tile by
-    // tile: while a tile's softmax works on one block, its next scores wait
-    // in tensor memory and the tensor cores work for the other tile.
-    for (int j = -1; j < n; ++j) {
-      const bool next = j + 1 < n;
-      int vs = 0, v_phase = 0;
-      if (j >= 0) {
-        vs = slot;
-        v_phase = phase;
-        advance(slot, phase);
-      }
-      const int ks = slot;
-      Steps st;
-      if (j >= 0) st = steps_of<T>(a, span, span.block(s.beg + j) * T);
-      if (next && !wait(C::B_FULL + ks, phase, kErrWaitFull)) return;
-      for (int t = 0; t < tiles; ++t) {
-        if (next) {
-          if (!scores(t, NT == 2 ? t : (s_n[0] + s_n[1]) & 1, ks)) return;
-          if (t + 1 == tiles && elect_one()) {
-            mma_commit(bars + 8 * (C::B_EMPTY + ks));
-            if (j + 2 == n) mma_commit(bars + 8 * C::B_QEMPTY);
+    for (int j = 0; j < w.n; ++j) {
+      if (!wait(C::B_FULL + slot, phase, kErrWaitFull)) return;
+      const uint32_t k = smem_desc_lo(sbase + slot * C::kSlotBytes, 16);
+      for (int t = 0; t < w.tiles; ++t) {
+        const int i = NT == 2 ? t : (s_n[0] + s_n[1]) & 1;
+        const int before = C::NS == 1 ? last : i;
+        if (s_n[before] > 0 && !wait(C::B_SFREE + before, s_n[before] - 1, kErrWaitFull)) return;
+        tc_fence_after();
+        const uint32_t q = q_lo + t * (C::kQBytes / 16), d = tmem + (C::NS == 1 ? 0 : i * T);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss<kHi>(d, q + (kk / 4) * (kTileRows * 8) + (kk % 4) * 2, k + (kk / 4) * (T * 8) + (kk % 4) * 2, idesc, kk > 0);
+          mma_commit(bars + 8 * (C::B_SFULL + i));
+          if (t + 1 == w.tiles) {
+            mma_commit(bars + 8 * (C::B_EMPTY + slot));
+            if (j + 1 == w.n) mma_commit(bars + 8 * C::B_QEMPTY);
           }
-          __syncwarp();
         }
-        if (j >= 0) {
-          if (t == 0 && !wait(C::B_FULL + vs, v_phase, kErrWaitFull)) return;
-          if (!values(t, NT == 2 ? t : (p_n[0] + p_n[1]) & 1, vs, st.k0, st.k1, j == 0)) return;
-        }
+        __syncwarp();
+        ++s_n[i];
+        last = i;
       }
-      if (j >= 0 && elect_one()) mma_commit(bars + 8 * (C::B_EMPTY + vs));
-      __syncwarp();
-      if (next) advance(slot, phase);
+      slot += 2;  // past the block's values
+      if (slot >= C::kSlots) {
+        slot -= C::kSlots;
+        phase ^= 1;
+      }
+    }
+  }
+}
+
+// O_t += P V of every block and tile, over the 16-key steps that some query sees.
+template <int D, bool kBf16>
+__device__ void issue_values(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int lane) {
+  using C = Cfg<D>;
+  constexpr int T = C::T, NT = C::NT;
+  constexpr uint32_t kHi = smem_desc_hi(1024);
+  constexpr uint32_t kIdesc = mma_idesc<kBf16>(kTileRows, D, true);
+  const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
+  int slot = 1, phase = 0;  // ring slot of the next values, and its phase
+  int p_n[2] = {0, 0};      // blocks issued, by barrier as for the scores
+  auto wait = [&](int bar, int n, int code) { return warp_wait_bounded(bars + 8 * bar, n & 1, a.err, code, lane); };
+  Work w;
+  for (int seg_n = 0;; ++seg_n) {
+    if (!take_segment<D>(a, smem, seg_n, lane, w) || w.kind < 0) return;
+    for (int j = 0; j < w.n; ++j) {
+      const Steps st = steps_of<T>(a, w.span, w.span.block(w.beg + j) * T);
+      if (!wait(C::B_FULL + slot, phase, kErrWaitFull)) return;
+      const uint32_t v = smem_desc_lo(sbase + slot * C::kSlotBytes, T * 128);
+      for (int t = 0; t < w.tiles; ++t) {
+        const int i = NT == 2 ? t : (p_n[0] + p_n[1]) & 1;
+        const uint32_t o = tmem + C::kOCol + t * D, p = tmem + C::kPCol + i * (T / 2);
+        if (!wait(C::B_PREADY + i, p_n[i], kErrWaitFull)) return;
+        tc_fence_after();
+        if (elect_one()) {
+          if (st.k0 == 0 && st.k1 == T / 16) {
+#pragma unroll
+            for (int kk = 0; kk < T / 16; ++kk) mma_ts<kHi>(o, p + kk * 8, v + kk * 128, kIdesc, kk > 0 || j > 0);
+          } else {
+            for (int kk = st.k0; kk < st.k1; ++kk) mma_ts<kHi>(o, p + kk * 8, v + kk * 128, kIdesc, kk > st.k0 || j > 0);
+          }
+          mma_commit(bars + 8 * (C::B_OFULL + i));
+          if (t + 1 == w.tiles) mma_commit(bars + 8 * (C::B_EMPTY + slot));
+        }
+        __syncwarp();
+        ++p_n[i];
+      }
+      slot += 2;
+      if (slot >= C::kSlots) {
+        slot -= C::kSlots;
+        phase ^= 1;
+      }
     }
   }
 }
@@ -589,23 +601,42 @@ __device__ __forceinline__ float weights(const float (&x)[T], uint32_t none, flo
 }
 
 // ---------------------------------------------------------------------------
-// Softmax warpgroups: thread r of warpgroup t owns row r of tile t.
+// Softmax warps: two threads share row r of tile t, each with half of a
+// block's keys (and later half of the output's columns).
 // ---------------------------------------------------------------------------
 template <int D, bool kBf16>
-__device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int t, int warp, int lane) {
+__device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int t, int half, int warp,
+                        int lane) {
   using C = Cfg<D>;
-  constexpr int T = C::T, NT = C::NT;
+  constexpr int T = C::T, NT = C::NT, TH = T / 2, DH = D / 2;
   const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
   const Segment *descs = reinterpret_cast<const Segment *>(smem + C::kDescOff);
   const int r = warp * 32 + lane;                        // row of the tile
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;    // this warp's lanes of tensor memory
-  const uint32_t o_addr = tmem + lanes + C::kOCol + t * D;
+  const uint32_t o_addr = tmem + lanes + C::kOCol + t * D + half * DH;
+  uint8_t *stage = smem + C::kStageOff + ((t * 2 + half) * 4 + warp) * 2048;
+  const uint8_t *other = smem + C::kStageOff + ((t * 2 + (half ^ 1)) * 4 + warp) * 2048;
+  const int xchg = C::B_XCHG + t * 4 + warp;
+  int x_n = 0;  // exchanges with the warp that has the rows' other halves
   // The issuing warp has negated the scores for a negative scale.  A zero scale
   // becomes one that leaves nothing of a score, since -inf marks a masked one.
   const float sl2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
   int seg_n = 0, blk_n = 0;   // segments and score blocks seen
   int slot_n = 1;             // ring slot, of all so far, that holds the current block's values
   auto wait = [&](int bar, int n, int code) { return warp_wait_bounded(bars + 8 * bar, n & 1, a.err, code, lane); };
+  // v of the row's other half.  The places alternate: a warp writes one again
+  // only after the exchange in between, which the other warp enters having
+  // read it.
+  auto exchange = [&](float v, float &v_other) {
+    const int at = (x_n & 1) * 128 + lane * 4;
+    *reinterpret_cast<float *>(stage + at) = v;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * xchg);
+    if (!wait(xchg, x_n, kErrWaitQ)) return false;
+    ++x_n;
+    v_other = *reinterpret_cast<const volatile float *>(other + at);
+    return true;
+  };
 
   for (;;) {
     const int d = seg_n % kDescs;
@@ -641,9 +672,9 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
       tc_fence_after();
       ++blk_n;
       const uint32_t s_addr = tmem + lanes + (C::NS == 1 ? 0 : u * T);
-      float x[T];
+      float x[TH];
 #pragma unroll
-      for (int c = 0; c < T; c += 32) tmem_ld32(s_addr + c, reinterpret_cast<uint32_t *>(x + c));
+      for (int c = 0; c < TH; c += 32) tmem_ld32(s_addr + half * TH + c, reinterpret_cast<uint32_t *>(x + c));
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
@@ -652,11 +683,11 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
       // The keys that this warp's rows see, 32 at a time: all, none or some.
       // Only a block at an edge of the masks looks.
       const bool edge = j0 + T > tile_lim || (j0 < tile_low && j0 + T > a.sinks);
-      uint32_t none = 0;  // bit c: keys 32 c .. 32 c + 31 are hidden from all rows of the warp
+      uint32_t none = 0;  // bit c: this half's keys 32 c .. 32 c + 31 are hidden from all rows of the warp
       if (edge) {
 #pragma unroll
-        for (int c = 0; c < T; c += 32) {
-          const int j = j0 + c;
+        for (int c = 0; c < TH; c += 32) {
+          const int j = j0 + half * TH + c;
           const uint32_t seen = bits_below(lim - j) & (~bits_below(low - j) | bits_below(a.sinks - j));
           if (!__any_sync(0xffffffffu, seen != 0)) {
             none |= 1u << (c / 32);
@@ -666,7 +697,10 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
           }
         }
       }
-      const float top = (edge ? row_max<T, true>(x, none) : row_max<T, false>(x, 0)) * sl2;
+      const float mine = edge ? row_max<TH, true>(x, none) : row_max<TH, false>(x, 0);
+      float theirs;
+      if (!exchange(mine, theirs)) return;
+      const float top = fmaxf(mine, theirs) * sl2;
       // The reference m follows the maximum only once it is 2^8 behind, so
       // the accumulator is hardly ever rescaled; weights stay below 2^8.
       const bool behind = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
@@ -681,7 +715,7 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
           if (!wait(C::B_OFULL + pu, pn, kErrWaitFull)) return;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
+          for (int c = 0; c < DH; c += 16) {
             float o[16];
             tmem_ld16(o_addr + c, reinterpret_cast<uint32_t *>(o));
             tmem_wait_ld();
@@ -698,7 +732,7 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
             const int sl = slot_n % C::kSlots;
             if (!wait(C::B_FULL + sl, slot_n / C::kSlots, kErrWaitFull)) return;
             const uint32_t v = sbase + sl * C::kSlotBytes;
-            for (int i = st.k0 * 16 * (D / 8) + r; i < st.k1 * 16 * (D / 8); i += kTileRows) {
+            for (int i = st.k0 * 16 * (D / 8) + half * kTileRows + r; i < st.k1 * 16 * (D / 8); i += 2 * kTileRows) {
               const int key = i / (D / 8), c = i % (D / 8);
               if (key >= st.top || (key >= st.g0 && key < st.g1))
                 asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + (c / 8) * (T * 128) + key * 128 + (c % 8) * 16),
@@ -711,14 +745,14 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
         slot_n += 2;
       }
       const float base = m == -INFINITY ? 0.f : -m;
-      uint32_t p[T / 2];
-      l += edge ? weights<T, kBf16, true>(x, none, sl2, base, p) : weights<T, kBf16, false>(x, 0, sl2, base, p);
+      uint32_t p[TH / 2];
+      l += edge ? weights<TH, kBf16, true>(x, none, sl2, base, p) : weights<TH, kBf16, false>(x, 0, sl2, base, p);
       // the product that read the buffer's weights before is done
       if (un > 0 && !wait(C::B_OFULL + u, un - 1, kErrWaitFull)) return;
       tc_fence_after();
-      const uint32_t p_addr = tmem + lanes + C::kPCol + u * (T / 2);
+      const uint32_t p_addr = tmem + lanes + C::kPCol + u * (T / 2) + half * (TH / 2);
 #pragma unroll
-      for (int c = 0; c < T / 2; c += 16) tmem_st16(p_addr + c, p + c);
+      for (int c = 0; c < TH / 2; c += 16) tmem_st16(p_addr + c, p + c);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -729,6 +763,11 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     const int lu = NT == 2 ? t : (blk_n - 1) & 1;  // the last block's values
     if (!wait(C::B_OFULL + lu, NT == 2 ? blk_n - 1 : (blk_n - 1) >> 1, kErrWaitFull)) return;
     tc_fence_after();
+    float l_other;
+    if (!exchange(l, l_other)) return;
+    l = half == 0 ? l + l_other : l_other + l;  // the same sum in both halves
+    // and once more, before the rows overwrite the place of the sums
+    if (!exchange(0.f, l_other)) return;
     const float inv = 1.f / l;
     const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     const int hq = s.h * a.G + r % a.G;
@@ -736,47 +775,49 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     const int out_row = (s.q0 + tok) * a.Hq + hq;
     const int piece_row = (blockIdx.x * 2 + (s.kind - 1)) * (NT * kTileRows) + t * kTileRows + r;
     const int row = !real ? -1 : s.kind == 0 ? out_row : piece_row;
-    uint8_t *stage = smem + C::kStageOff + (t * 4 + warp) * 4096;
     uint8_t *dst = s.kind == 0 ? static_cast<uint8_t *>(a.out) : reinterpret_cast<uint8_t *>(a.o_part);
     const int pitch = s.kind == 0 ? D * 2 : D * 4;  // bytes of a row
-    // 128 bytes of every row at a time, through shared memory (16-byte chunks
-    // swizzled by the row), so that 8 lanes write a row's bytes together: a
+    // 64 bytes of every row at a time, through shared memory (16-byte chunks
+    // swizzled by the row), so that 4 lanes write a row's bytes together: a
     // lane writing its own row would touch 32 lines with every store.
     auto flush = [&](int at) {
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int rr = i * 4 + (lane >> 3), c = lane & 7;
+      for (int i = 0; i < 4; ++i) {
+        const int rr = i * 8 + (lane >> 2), c = lane & 3;
         const int to = __shfl_sync(0xffffffffu, row, rr);
-        const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
+        const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
         if (to >= 0) *reinterpret_cast<uint4 *>(dst + (size_t)to * pitch + at + c * 16) = v;
       }
       __syncwarp();
     };
-    auto put = [&](int c, uint4 v) { *reinterpret_cast<uint4 *>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = v; };
+    auto put = [&](int c, uint4 v) { *reinterpret_cast<uint4 *>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = v; };
+    __syncwarp();
 #pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
+    for (int c = 0; c < DH; c += 32) {
       float o[32];
       tmem_ld32(o_addr + c, reinterpret_cast<uint32_t *>(o));
       tmem_wait_ld();
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;  // no key: O holds nothing to read
       if (s.kind == 0) {
-        const int half = (c >> 5) & 1;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          put(half * 4 + i, make_uint4(pack2<kBf16>(o[8 * i], o[8 * i + 1]), pack2<kBf16>(o[8 * i + 2], o[8 * i + 3]),
-                                       pack2<kBf16>(o[8 * i + 4], o[8 * i + 5]), pack2<kBf16>(o[8 * i + 6], o[8 * i + 7])));
-        if (half) flush((c - 32) * 2);
+          put(i, make_uint4(pack2<kBf16>(o[8 * i], o[8 * i + 1]), pack2<kBf16>(o[8 * i + 2], o[8 * i + 3]),
+                            pack2<kBf16>(o[8 * i + 4], o[8 * i + 5]), pack2<kBf16>(o[8 * i + 6], o[8 * i + 7])));
+        flush((half * DH + c) * 2);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          put(i, make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
-                            __float_as_uint(o[4 * i + 3])));
-        flush(c * 4);
+        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            put(i, make_uint4(__float_as_uint(o[16 * q + 4 * i]), __float_as_uint(o[16 * q + 4 * i + 1]),
+                              __float_as_uint(o[16 * q + 4 * i + 2]), __float_as_uint(o[16 * q + 4 * i + 3])));
+          flush((half * DH + c + 16 * q) * 4);
+        }
       }
     }
-    if (real) {
+    if (real && half == 0) {
       if (s.kind == 0) {
         if (a.lse != nullptr) a.lse[(size_t)hq * a.total_q + s.q0 + tok] = lse;
       } else {
@@ -784,7 +825,7 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
       }
     }
     // the head piece's description, for the merge
-    if (s.kind == 1 && t == 0 && r == 0) {
+    if (s.kind == 1 && t == 0 && half == 0 && r == 0) {
       PieceDesc &pd = a.pieces[blockIdx.x];
       pd.q0 = s.q0;
       pd.h = s.h;
@@ -816,19 +857,20 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars + 8 * (C::B_SFULL + i), 1);
-      mbar_init(bars + 8 * (C::B_SFREE + i), 4);  // one arrival a softmax warp
-      mbar_init(bars + 8 * (C::B_PREADY + i), 4);
+      mbar_init(bars + 8 * (C::B_SFREE + i), 8);  // one arrival a softmax warp of the tile
+      mbar_init(bars + 8 * (C::B_PREADY + i), 8);
       mbar_init(bars + 8 * (C::B_OFULL + i), 1);
     }
     mbar_init(bars + 8 * C::B_QFULL, 1);
     mbar_init(bars + 8 * C::B_QEMPTY, 1);
     for (int i = 0; i < kDescs; ++i) {
       mbar_init(bars + 8 * (C::B_DFULL + i), 1);
-      mbar_init(bars + 8 * (C::B_DEMPTY + i), C::kSoftmaxWarps + 2);
+      mbar_init(bars + 8 * (C::B_DEMPTY + i), C::kSoftmaxWarps + 3);
     }
+    for (int i = 0; i < 4 * C::NT; ++i) mbar_init(bars + 8 * (C::B_XCHG + i), 2);
     fence_mbar_init();
   }
-  if (warp == C::kMmaWarp) tmem_alloc(tmem_slot, 512);
+  if (warp == C::kScoreWarp) tmem_alloc(tmem_slot, 512);
   grid_launch_dependents();
   // Inputs may be written, and outputs and workspace used, by the kernel
   // this launch depends on.
@@ -853,18 +895,19 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
   tmem = __shfl_sync(0xffffffffu, tmem, 0);
   if (warp >= C::kSoftmaxWarps) {
-    if constexpr (C::NT == 2) regs_dec<88>();  // 168 a thread at launch: 384 x 168 = 256 x 208 + 128 x 88
-    if (warp == C::kMmaWarp) issuer<D, kBf16>(a, smem, tmem, lane);
+    if constexpr (C::NT == 2) regs_dec<64>();  // 96 a thread at launch: 640 x 96 = 512 x 104 + 128 x 64
+    if (warp == C::kScoreWarp) issue_scores<D, kBf16>(a, smem, tmem, lane);
+    else if (warp == C::kValueWarp) issue_values<D, kBf16>(a, smem, tmem, lane);
     else if (warp == C::kProducerWarp) producer<D, kBf16>(tm, a, smem, lane);
     else if (warp == C::kQueryWarp) queries<D>(tm, a, smem, lane);
   } else {
-    if constexpr (C::NT == 2) regs_inc<208>();
-    softmax<D, kBf16>(a, smem, tmem, warp / 4, warp % 4, lane);
+    if constexpr (C::NT == 2) regs_inc<104>();
+    softmax<D, kBf16>(a, smem, tmem, warp / 8, (warp / 4) % 2, warp % 4, lane);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == C::kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == C::kScoreWarp) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
