@@ -46,7 +46,7 @@ struct Cfg {
   static constexpr int CH = D / 64;                 // 64-column chunks of a row
   static constexpr int kSoftmaxWarps = 8 * NT;      // two threads a row
   static constexpr int kScoreWarp = kSoftmaxWarps, kValueWarp = kSoftmaxWarps + 1;
-  static constexpr int kProducerWarp = kSoftmaxWarps + 2, kQueryWarp = kSoftmaxWarps + 3;
+  static constexpr int kProducerWarp = kSoftmaxWarps + 2;  // and the query warp
   static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
   static constexpr int kSlotBytes = T * D * 2;      // one block of K or of V
   static constexpr int kSlots = 128 * 1024 / kSlotBytes;  // even: keys in the even slots, values in the odd ones
@@ -266,11 +266,27 @@ __device__ Walk walk_start(const PrefillArgs &a, int *rows, int lane) {
   return w;
 }
 
+// Bounded wait of every lane of a warp for the phase of `bar` with this
+// parity; false when it has run out (the role then ends, and its warp records
+// the failure).  Few instructions, since every wait is a copy of them.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
+  bool done = mbar_try_wait(bar, parity);
+  if (!done) {
+    uint32_t t0, t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t0));
+    do {
+      done = mbar_try_wait(bar, parity);
+      asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    } while (!done && t - t0 < (uint32_t)kWaitLimitNs);
+  }
+  return __all_sync(0xffffffffu, done);
+}
+
 // ---------------------------------------------------------------------------
 // Producer warp
 // ---------------------------------------------------------------------------
 template <int D, bool kBf16>
-__device__ void producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *smem, int lane) {
+__device__ bool producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *smem, int lane) {
   using C = Cfg<D>;
   constexpr int T = C::T;
   const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
@@ -297,7 +313,7 @@ __device__ void producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *s
     if (more) s = walk_take<D>(a, w);
     else s.kind = -1;
     const int d = seg_n % kDescs;
-    if (!warp_wait_bounded(bars + 8 * (C::B_DEMPTY + d), ((seg_n / kDescs) & 1) ^ 1, a.err, kErrWaitQ, lane)) {
+    if (!wait_phase(bars + 8 * (C::B_DEMPTY + d), ((seg_n / kDescs) & 1) ^ 1)) {
       ok = false;
       break;
     }
@@ -321,7 +337,7 @@ __device__ void producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *s
       for (int kv = 0; kv < 2; ++kv) {
         const int sl = slot_n % C::kSlots;
         const uint32_t full = bars + 8 * (C::B_FULL + sl);
-        if (!warp_wait_bounded(bars + 8 * (C::B_EMPTY + sl), ((slot_n / C::kSlots) & 1) ^ 1, a.err, kErrWaitEmpty, lane)) {
+        if (!wait_phase(bars + 8 * (C::B_EMPTY + sl), ((slot_n / C::kSlots) & 1) ^ 1)) {
           ok = false;
           break;
         }
@@ -356,7 +372,8 @@ __device__ void producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *s
   if (__any_sync(0xffffffffu, bad_page) && lane == 0) atomicOr(a.err, kErrBadPage);
   // Leave only when the copies issued here have landed.
   for (int j = max(0, slot_n - C::kSlots); j < slot_n; ++j)
-    mbar_wait_bounded(bars + 8 * (C::B_FULL + j % C::kSlots), (j / C::kSlots) & 1, a.err, kErrDrain);
+    ok &= wait_phase(bars + 8 * (C::B_FULL + j % C::kSlots), (j / C::kSlots) & 1);
+  return ok;
 }
 
 // ---------------------------------------------------------------------------
@@ -365,21 +382,22 @@ __device__ void producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *s
 // values are on their way before that.
 // ---------------------------------------------------------------------------
 template <int D>
-__device__ void queries(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *smem, int lane) {
+__device__ bool queries(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *smem, int lane) {
   using C = Cfg<D>;
   constexpr int NT = C::NT;
   const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
   const Segment *descs = reinterpret_cast<const Segment *>(smem + C::kDescOff);
   if (lane == 0) prefetch_tmap(&tm.q);
   int seg_n = 0;
+  bool ok = true;
   for (;; ++seg_n) {
     const int d = seg_n % kDescs;
-    if (!warp_wait_bounded(bars + 8 * (C::B_DFULL + d), (seg_n / kDescs) & 1, a.err, kErrWaitQ, lane)) break;
+    if (!(ok = wait_phase(bars + 8 * (C::B_DFULL + d), (seg_n / kDescs) & 1))) break;
     const Segment s = descs[d];
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * (C::B_DEMPTY + d));
     if (s.kind < 0) break;
-    if (!warp_wait_bounded(bars + 8 * C::B_QEMPTY, (seg_n & 1) ^ 1, a.err, kErrWaitQ, lane)) break;
+    if (!(ok = wait_phase(bars + 8 * C::B_QEMPTY, (seg_n & 1) ^ 1))) break;
     const int t0 = s.it * NT * a.TQ;
     const int tiles = min(NT, (s.qn - t0 + a.TQ - 1) / a.TQ);
     if (lane == 0) mbar_arrive_expect_tx(bars + 8 * C::B_QFULL, (uint32_t)(tiles * C::CH * a.TQ * a.G * 128));
@@ -391,7 +409,8 @@ __device__ void queries(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *sm
     }
   }
   // leave only when the copies issued here have landed
-  if (seg_n > 0) mbar_wait_bounded(bars + 8 * C::B_QFULL, (seg_n - 1) & 1, a.err, kErrDrain);
+  if (seg_n > 0) ok &= wait_phase(bars + 8 * C::B_QFULL, (seg_n - 1) & 1);
+  return ok;
 }
 
 // Keys of the block at tok0 that some query of the unit may see, as the
@@ -435,7 +454,7 @@ __device__ __forceinline__ bool take_segment(const PrefillArgs &a, uint8_t *smem
   using C = Cfg<D>;
   const uint32_t bars = smem_addr(smem) + C::kBarOff;
   const int d = seg_n % kDescs;
-  if (!warp_wait_bounded(bars + 8 * (C::B_DFULL + d), (seg_n / kDescs) & 1, a.err, kErrWaitQ, lane)) return false;
+  if (!wait_phase(bars + 8 * (C::B_DFULL + d), (seg_n / kDescs) & 1)) return false;
   const Segment *s = reinterpret_cast<const Segment *>(smem + C::kDescOff) + d;
   w.kind = __shfl_sync(0xffffffffu, s->kind, 0);
   const int it = __shfl_sync(0xffffffffu, s->it, 0), qn = __shfl_sync(0xffffffffu, s->qn, 0);
@@ -453,7 +472,7 @@ __device__ __forceinline__ bool take_segment(const PrefillArgs &a, uint8_t *smem
 // buffer are in registers: a tile's next scores wait in tensor memory while
 // its softmax works on a block.
 template <int D, bool kBf16>
-__device__ void issue_scores(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int lane) {
+__device__ bool issue_scores(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int lane) {
   using C = Cfg<D>;
   constexpr int T = C::T, NT = C::NT;
   constexpr uint32_t kHi = smem_desc_hi(1024);
@@ -466,18 +485,19 @@ __device__ void issue_scores(const PrefillArgs &a, uint8_t *smem, uint32_t tmem,
   // tile the even and the odd ones
   int s_n[2] = {0, 0};
   int last = 0;  // the tile (or parity) whose scores were issued last
-  auto wait = [&](int bar, int n, int code) { return warp_wait_bounded(bars + 8 * bar, n & 1, a.err, code, lane); };
+  auto wait = [&](int bar, int n) { return wait_phase(bars + 8 * bar, n & 1); };
   Work w;
   for (int seg_n = 0;; ++seg_n) {
-    if (!take_segment<D>(a, smem, seg_n, lane, w) || w.kind < 0) return;
-    if (!wait(C::B_QFULL, seg_n, kErrWaitQ)) return;
+    if (!take_segment<D>(a, smem, seg_n, lane, w)) return false;
+    if (w.kind < 0) return true;
+    if (!wait(C::B_QFULL, seg_n)) return false;
     for (int j = 0; j < w.n; ++j) {
-      if (!wait(C::B_FULL + slot, phase, kErrWaitFull)) return;
+      if (!wait(C::B_FULL + slot, phase)) return false;
       const uint32_t k = smem_desc_lo(sbase + slot * C::kSlotBytes, 16);
       for (int t = 0; t < w.tiles; ++t) {
         const int i = NT == 2 ? t : (s_n[0] + s_n[1]) & 1;
         const int before = C::NS == 1 ? last : i;
-        if (s_n[before] > 0 && !wait(C::B_SFREE + before, s_n[before] - 1, kErrWaitFull)) return;
+        if (s_n[before] > 0 && !wait(C::B_SFREE + before, s_n[before] - 1)) return false;
         tc_fence_after();
         const uint32_t q = q_lo + t * (C::kQBytes / 16), d = tmem + (C::NS == 1 ? 0 : i * T);
         if (elect_one()) {
@@ -505,7 +525,7 @@ __device__ void issue_scores(const PrefillArgs &a, uint8_t *smem, uint32_t tmem,
 
 // O_t += P V of every block and tile, over the 16-key steps that some query sees.
 template <int D, bool kBf16>
-__device__ void issue_values(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int lane) {
+__device__ bool issue_values(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int lane) {
   using C = Cfg<D>;
   constexpr int T = C::T, NT = C::NT;
   constexpr uint32_t kHi = smem_desc_hi(1024);
@@ -513,18 +533,19 @@ __device__ void issue_values(const PrefillArgs &a, uint8_t *smem, uint32_t tmem,
   const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
   int slot = 1, phase = 0;  // ring slot of the next values, and its phase
   int p_n[2] = {0, 0};      // blocks issued, by barrier as for the scores
-  auto wait = [&](int bar, int n, int code) { return warp_wait_bounded(bars + 8 * bar, n & 1, a.err, code, lane); };
+  auto wait = [&](int bar, int n) { return wait_phase(bars + 8 * bar, n & 1); };
   Work w;
   for (int seg_n = 0;; ++seg_n) {
-    if (!take_segment<D>(a, smem, seg_n, lane, w) || w.kind < 0) return;
+    if (!take_segment<D>(a, smem, seg_n, lane, w)) return false;
+    if (w.kind < 0) return true;
     for (int j = 0; j < w.n; ++j) {
       const Steps st = steps_of<T>(a, w.span, w.span.block(w.beg + j) * T);
-      if (!wait(C::B_FULL + slot, phase, kErrWaitFull)) return;
+      if (!wait(C::B_FULL + slot, phase)) return false;
       const uint32_t v = smem_desc_lo(sbase + slot * C::kSlotBytes, T * 128);
       for (int t = 0; t < w.tiles; ++t) {
         const int i = NT == 2 ? t : (p_n[0] + p_n[1]) & 1;
         const uint32_t o = tmem + C::kOCol + t * D, p = tmem + C::kPCol + i * (T / 2);
-        if (!wait(C::B_PREADY + i, p_n[i], kErrWaitFull)) return;
+        if (!wait(C::B_PREADY + i, p_n[i])) return false;
         tc_fence_after();
         if (elect_one()) {
           if (st.k0 == 0 && st.k1 == T / 16) {
@@ -553,65 +574,18 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
-// Maximum of a row's scores, but for the groups of 32 in `none` (kEdge only;
-// a block away from every edge is straight-line code).
-template <int T, bool kEdge>
-__device__ __forceinline__ float row_max(const float (&x)[T], uint32_t none) {
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int c = 0; c < T; c += 32) {
-    if (kEdge && ((none >> (c / 32)) & 1u)) continue;
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], x[c + i], x[c + i + 1]);
-  }
-  return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-}
-
-// Of kPolyOf pairs of weights, kPoly are computed on the floating-point pipe.
-constexpr int kPoly = 0, kPolyOf = 4;
-
-// The row's weights 2^(scale x + base), rounded to the input type, two in a
-// word; returns their sum (before the rounding).
-template <int T, bool kBf16, bool kEdge>
-__device__ __forceinline__ float weights(const float (&x)[T], uint32_t none, float scale, float base, uint32_t (&p)[T / 2]) {
-  const float2 sc = make_float2(scale, scale), bs = make_float2(base, base);
-  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-  for (int c = 0; c < T; c += 32) {
-    if (kEdge && ((none >> (c / 32)) & 1u)) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) p[c / 2 + i] = 0u;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        float2 e = fma2(make_float2(x[c + i], x[c + i + 1]), sc, bs);
-        if (!kEdge && (i >> 1) % kPolyOf < kPoly) {
-          e = ex2_poly(e);
-        } else {
-          e.x = ex2(e.x);
-          e.y = ex2(e.y);
-        }
-        sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
-        p[(c + i) / 2] = pack2<kBf16>(e.x, e.y);
-      }
-    }
-  }
-  sum[0] = add2(sum[0], sum[1]);
-  return sum[0].x + sum[0].y;
-}
-
 // ---------------------------------------------------------------------------
 // Softmax warps: two threads share row r of tile t, each with half of a
 // block's keys (and later half of the output's columns).
 // ---------------------------------------------------------------------------
 template <int D, bool kBf16>
-__device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int t, int half, int warp,
-                        int lane) {
+__device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int t, int half, int warp, int lane) {
   using C = Cfg<D>;
   constexpr int T = C::T, NT = C::NT, TH = T / 2, DH = D / 2;
   const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
   const Segment *descs = reinterpret_cast<const Segment *>(smem + C::kDescOff);
-  const int r = warp * 32 + lane;                        // row of the tile
+  const int r = warp * 32 + lane;                        // row of the tile:
+  const int r_tok = r / a.G, r_head = r - r_tok * a.G;   // its token and head
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;    // this warp's lanes of tensor memory
   const uint32_t o_addr = tmem + lanes + C::kOCol + t * D + half * DH;
   uint8_t *stage = smem + C::kStageOff + ((t * 2 + half) * 4 + warp) * 2048;
@@ -623,7 +597,7 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
   const float sl2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
   int seg_n = 0, blk_n = 0;   // segments and score blocks seen
   int slot_n = 1;             // ring slot, of all so far, that holds the current block's values
-  auto wait = [&](int bar, int n, int code) { return warp_wait_bounded(bars + 8 * bar, n & 1, a.err, code, lane); };
+  auto wait = [&](int bar, int n) { return wait_phase(bars + 8 * bar, n & 1); };
   // v of the row's other half.  The places alternate: a warp writes one again
   // only after the exchange in between, which the other warp enters having
   // read it.
@@ -632,7 +606,7 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     *reinterpret_cast<float *>(stage + at) = v;
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * xchg);
-    if (!wait(xchg, x_n, kErrWaitQ)) return false;
+    if (!wait(xchg, x_n)) return false;
     ++x_n;
     v_other = *reinterpret_cast<const volatile float *>(other + at);
     return true;
@@ -640,20 +614,20 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
 
   for (;;) {
     const int d = seg_n % kDescs;
-    if (!wait(C::B_DFULL + d, seg_n / kDescs, kErrWaitQ)) return;
+    if (!wait(C::B_DFULL + d, seg_n / kDescs)) return false;
     const Segment s = descs[d];
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * (C::B_DEMPTY + d));
     ++seg_n;
-    if (s.kind < 0) return;
+    if (s.kind < 0) return true;
     const int u0 = s.it * NT * a.TQ, tt0 = u0 + t * a.TQ;  // first token of the unit and of this tile
     if (tt0 >= s.qn) {                                      // the unit's second tile is empty
       slot_n += 2 * (s.end - s.beg);
       continue;
     }
     const Span span = span_of<T>(a, s.L, s.qn, u0, min(u0 + NT * a.TQ, s.qn));
-    const int tok = tt0 + r / a.G;
-    const bool real = r < a.TQ * a.G && tok < s.qn;
+    const int tok = tt0 + r_tok;
+    const bool real = r_tok < a.TQ && tok < s.qn;
     // keys this row sees: [0, sinks) and [low, lim)
     int lim = a.causal ? min(s.L, s.L - s.qn + tok + 1) : s.L;
     if (!real) lim = 0;
@@ -668,38 +642,50 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     for (int blk = s.beg; blk < s.end; ++blk) {
       // barriers: the tile's, or with one tile those of the block's parity
       const int u = NT == 2 ? t : blk_n & 1, un = NT == 2 ? blk_n : blk_n >> 1;
-      if (!wait(C::B_SFULL + u, un, kErrWaitFull)) return;
+      if (!wait(C::B_SFULL + u, un)) return false;
       tc_fence_after();
       ++blk_n;
-      const uint32_t s_addr = tmem + lanes + (C::NS == 1 ? 0 : u * T);
+      const uint32_t s_addr = tmem + lanes + (C::NS == 1 ? 0 : u * T) + half * TH;
       float x[TH];
 #pragma unroll
-      for (int c = 0; c < TH; c += 32) tmem_ld32(s_addr + half * TH + c, reinterpret_cast<uint32_t *>(x + c));
+      for (int c = 0; c < TH; c += 32) tmem_ld32(s_addr + c, reinterpret_cast<uint32_t *>(x + c));
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * (C::B_SFREE + u));
       const int j0 = span.block(blk) * T;
-      // The keys that this warp's rows see, 32 at a time: all, none or some.
-      // Only a block at an edge of the masks looks.
-      const bool edge = j0 + T > tile_lim || (j0 < tile_low && j0 + T > a.sinks);
-      uint32_t none = 0;  // bit c: this half's keys 32 c .. 32 c + 31 are hidden from all rows of the warp
-      if (edge) {
+      if (j0 + T > tile_lim || (j0 < tile_low && j0 + T > a.sinks)) {
+        // one bit a key: seen or not
 #pragma unroll
         for (int c = 0; c < TH; c += 32) {
           const int j = j0 + half * TH + c;
           const uint32_t seen = bits_below(lim - j) & (~bits_below(low - j) | bits_below(a.sinks - j));
-          if (!__any_sync(0xffffffffu, seen != 0)) {
-            none |= 1u << (c / 32);
-          } else if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[c + i] = (seen >> i) & 1u ? x[c + i] : -INFINITY;
+          for (int i = 0; i < 32; ++i) x[c + i] = (seen >> i) & 1u ? x[c + i] : -INFINITY;
+        }
+        const Steps st = steps_of<T>(a, span, j0);
+        if (t == 0 && st.clear) {  // values of hidden keys become zeros
+          const int sl = slot_n % C::kSlots;
+          if (!wait(C::B_FULL + sl, slot_n / C::kSlots)) return false;
+          const uint32_t v = sbase + sl * C::kSlotBytes;
+#pragma unroll 1
+          for (int i = st.k0 * 16 * (D / 8) + half * kTileRows + r; i < st.k1 * 16 * (D / 8); i += 2 * kTileRows) {
+            const int key = i / (D / 8), c = i % (D / 8);
+            if (key >= st.top || (key >= st.g0 && key < st.g1))
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + (c / 8) * (T * 128) + key * 128 + (c % 8) * 16),
+                           "r"(0u) : "memory");
           }
+          fence_proxy_async_smem();  // before the product reads them
+          __syncwarp();
         }
       }
-      const float mine = edge ? row_max<TH, true>(x, none) : row_max<TH, false>(x, 0);
+      slot_n += 2;
+      float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int i = 4; i < TH; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], x[i], x[i + 1]);
+      const float mine = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
       float theirs;
-      if (!exchange(mine, theirs)) return;
+      if (!exchange(mine, theirs)) return false;
       const float top = fmaxf(mine, theirs) * sl2;
       // The reference m follows the maximum only once it is 2^8 behind, so
       // the accumulator is hardly ever rescaled; weights stay below 2^8.
@@ -712,7 +698,7 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
         if (blk > s.beg) {
           // the values of the block before are in the accumulator
           const int pu = NT == 2 ? t : u ^ 1, pn = NT == 2 ? un - 1 : (blk_n - 2) >> 1;
-          if (!wait(C::B_OFULL + pu, pn, kErrWaitFull)) return;
+          if (!wait(C::B_OFULL + pu, pn)) return false;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < DH; c += 16) {
@@ -725,30 +711,24 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
           }
         }
       }
-      if (t == 0) {
-        if (edge) {
-          const Steps st = steps_of<T>(a, span, j0);
-          if (st.clear) {  // values of hidden keys become zeros
-            const int sl = slot_n % C::kSlots;
-            if (!wait(C::B_FULL + sl, slot_n / C::kSlots, kErrWaitFull)) return;
-            const uint32_t v = sbase + sl * C::kSlotBytes;
-            for (int i = st.k0 * 16 * (D / 8) + half * kTileRows + r; i < st.k1 * 16 * (D / 8); i += 2 * kTileRows) {
-              const int key = i / (D / 8), c = i % (D / 8);
-              if (key >= st.top || (key >= st.g0 && key < st.g1))
-                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + (c / 8) * (T * 128) + key * 128 + (c % 8) * 16),
-                             "r"(0u) : "memory");
-            }
-            fence_proxy_async_smem();  // before the product reads them
-            __syncwarp();
-          }
-        }
-        slot_n += 2;
-      }
+      // weights 2^(scale x - m), rounded to the input type, two in a word;
+      // their sum is taken before the rounding
       const float base = m == -INFINITY ? 0.f : -m;
+      const float2 sc = make_float2(sl2, sl2), bs = make_float2(base, base);
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       uint32_t p[TH / 2];
-      l += edge ? weights<TH, kBf16, true>(x, none, sl2, base, p) : weights<TH, kBf16, false>(x, 0, sl2, base, p);
+#pragma unroll
+      for (int i = 0; i < TH; i += 2) {
+        float2 e = fma2(make_float2(x[i], x[i + 1]), sc, bs);
+        e.x = ex2(e.x);
+        e.y = ex2(e.y);
+        sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
+        p[i >> 1] = pack2<kBf16>(e.x, e.y);
+      }
+      sum[0] = add2(sum[0], sum[1]);
+      l += sum[0].x + sum[0].y;
       // the product that read the buffer's weights before is done
-      if (un > 0 && !wait(C::B_OFULL + u, un - 1, kErrWaitFull)) return;
+      if (un > 0 && !wait(C::B_OFULL + u, un - 1)) return false;
       tc_fence_after();
       const uint32_t p_addr = tmem + lanes + C::kPCol + u * (T / 2) + half * (TH / 2);
 #pragma unroll
@@ -760,69 +740,21 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     }
 
     // ---- the rows: O / l and LSE ----
-    const int lu = NT == 2 ? t : (blk_n - 1) & 1;  // the last block's values
-    if (!wait(C::B_OFULL + lu, NT == 2 ? blk_n - 1 : (blk_n - 1) >> 1, kErrWaitFull)) return;
-    tc_fence_after();
     float l_other;
-    if (!exchange(l, l_other)) return;
+    if (!exchange(l, l_other)) return false;
     l = half == 0 ? l + l_other : l_other + l;  // the same sum in both halves
     // and once more, before the rows overwrite the place of the sums
-    if (!exchange(0.f, l_other)) return;
-    const float inv = 1.f / l;
-    const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    const int hq = s.h * a.G + r % a.G;
+    if (!exchange(0.f, l_other)) return false;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int hq = s.h * a.G + r_head;
     // Where the row goes: row `row` of the output, or of the CTA's piece slot.
-    const int out_row = (s.q0 + tok) * a.Hq + hq;
-    const int piece_row = (blockIdx.x * 2 + (s.kind - 1)) * (NT * kTileRows) + t * kTileRows + r;
-    const int row = !real ? -1 : s.kind == 0 ? out_row : piece_row;
-    uint8_t *dst = s.kind == 0 ? static_cast<uint8_t *>(a.out) : reinterpret_cast<uint8_t *>(a.o_part);
-    const int pitch = s.kind == 0 ? D * 2 : D * 4;  // bytes of a row
-    // 64 bytes of every row at a time, through shared memory (16-byte chunks
-    // swizzled by the row), so that 4 lanes write a row's bytes together: a
-    // lane writing its own row would touch 32 lines with every store.
-    auto flush = [&](int at) {
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int rr = i * 8 + (lane >> 2), c = lane & 3;
-        const int to = __shfl_sync(0xffffffffu, row, rr);
-        const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
-        if (to >= 0) *reinterpret_cast<uint4 *>(dst + (size_t)to * pitch + at + c * 16) = v;
-      }
-      __syncwarp();
-    };
-    auto put = [&](int c, uint4 v) { *reinterpret_cast<uint4 *>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = v; };
-    __syncwarp();
-#pragma unroll 1
-    for (int c = 0; c < DH; c += 32) {
-      float o[32];
-      tmem_ld32(o_addr + c, reinterpret_cast<uint32_t *>(o));
-      tmem_wait_ld();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;  // no key: O holds nothing to read
-      if (s.kind == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          put(i, make_uint4(pack2<kBf16>(o[8 * i], o[8 * i + 1]), pack2<kBf16>(o[8 * i + 2], o[8 * i + 3]),
-                            pack2<kBf16>(o[8 * i + 4], o[8 * i + 5]), pack2<kBf16>(o[8 * i + 6], o[8 * i + 7])));
-        flush((half * DH + c) * 2);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            put(i, make_uint4(__float_as_uint(o[16 * q + 4 * i]), __float_as_uint(o[16 * q + 4 * i + 1]),
-                              __float_as_uint(o[16 * q + 4 * i + 2]), __float_as_uint(o[16 * q + 4 * i + 3])));
-          flush((half * DH + c + 16 * q) * 4);
-        }
-      }
-    }
+    const int row0 = s.kind == 0 ? (s.q0 + tok) * a.Hq + hq
+                                 : (blockIdx.x * 2 + (s.kind - 1)) * (NT * kTileRows) + t * kTileRows + r;
+    const int row = real ? row0 : -1;
     if (real && half == 0) {
-      if (s.kind == 0) {
-        if (a.lse != nullptr) a.lse[(size_t)hq * a.total_q + s.q0 + tok] = lse;
-      } else {
-        a.lse_part[piece_row] = lse;
-      }
+      const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      if (s.kind != 0) a.lse_part[row0] = lse;
+      else if (a.lse != nullptr) a.lse[(size_t)hq * a.total_q + s.q0 + tok] = lse;
     }
     // the head piece's description, for the merge
     if (s.kind == 1 && t == 0 && half == 0 && r == 0) {
@@ -833,6 +765,45 @@ __device__ void softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
       pd.tokens = min(NT * a.TQ, s.qn - u0);
       pd.c_first = s.c_first;
       pd.n_pieces = s.n_pieces;
+    }
+    const int lu = NT == 2 ? t : (blk_n - 1) & 1;  // the last block's values
+    if (!wait(C::B_OFULL + lu, NT == 2 ? blk_n - 1 : (blk_n - 1) >> 1)) return false;
+    tc_fence_after();
+    // 16 columns of every row at a time, through shared memory (16-byte chunks
+    // swizzled by the row), so that 2 or 4 lanes write a row's bytes
+    // together: a lane writing its own row would touch 32 lines with every
+    // store.  A short loop: code that runs once a unit is fetched anew.
+    const bool piece = s.kind != 0;
+    const int shift = piece ? 2 : 1;  // log2 of a row's 16-byte chunks a step, and of a value's bytes
+    uint8_t *dst = (piece ? reinterpret_cast<uint8_t *>(a.o_part) : static_cast<uint8_t *>(a.out)) + ((half * DH) << shift);
+    const int c = lane & ((1 << shift) - 1);
+#pragma unroll 1
+    for (int col = 0; col < DH; col += 16) {
+      float o[16];
+      tmem_ld16(o_addr + col, reinterpret_cast<uint32_t *>(o));
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;  // no key: O holds nothing to read
+      __syncwarp();
+      if (piece) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4 *>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+              make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<uint4 *>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(pack2<kBf16>(o[8 * i], o[8 * i + 1]), pack2<kBf16>(o[8 * i + 2], o[8 * i + 3]),
+                         pack2<kBf16>(o[8 * i + 4], o[8 * i + 5]), pack2<kBf16>(o[8 * i + 6], o[8 * i + 7]));
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int rr = lane >> shift; rr < 32; rr += 32 >> shift) {
+        const int to = __shfl_sync(0xffffffffu, row, rr);
+        const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
+        if (to >= 0) *reinterpret_cast<uint4 *>(dst + (((size_t)to * D + col) << shift) + c * 16) = v;
+      }
     }
     tc_fence_before();  // the accumulator has been read before this thread's next arrival
   }
@@ -894,16 +865,18 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   uint32_t tmem;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
   tmem = __shfl_sync(0xffffffffu, tmem, 0);
+  bool ok;
   if (warp >= C::kSoftmaxWarps) {
     if constexpr (C::NT == 2) regs_dec<64>();  // 96 a thread at launch: 640 x 96 = 512 x 104 + 128 x 64
-    if (warp == C::kScoreWarp) issue_scores<D, kBf16>(a, smem, tmem, lane);
-    else if (warp == C::kValueWarp) issue_values<D, kBf16>(a, smem, tmem, lane);
-    else if (warp == C::kProducerWarp) producer<D, kBf16>(tm, a, smem, lane);
-    else if (warp == C::kQueryWarp) queries<D>(tm, a, smem, lane);
+    if (warp == C::kScoreWarp) ok = issue_scores<D, kBf16>(a, smem, tmem, lane);
+    else if (warp == C::kValueWarp) ok = issue_values<D, kBf16>(a, smem, tmem, lane);
+    else if (warp == C::kProducerWarp) ok = producer<D, kBf16>(tm, a, smem, lane);
+    else ok = queries<D>(tm, a, smem, lane);
   } else {
     if constexpr (C::NT == 2) regs_inc<104>();
-    softmax<D, kBf16>(a, smem, tmem, warp / 8, (warp / 4) % 2, warp % 4, lane);
+    ok = softmax<D, kBf16>(a, smem, tmem, warp / 8, (warp / 4) % 2, warp % 4, lane);
   }
+  if (!ok && lane == 0) atomicOr(a.err, kErrWaitFull);  // a wait ran out
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
