@@ -44,12 +44,17 @@ struct Cfg {
   static constexpr int NT = D <= 128 ? 2 : 1;       // tiles of a unit
   static constexpr int T = D <= 128 ? 128 : 64;     // keys of a block
   static constexpr int CH = D / 64;                 // 64-column chunks of a row
+  // A block of K or V in shared memory: groups of 8 keys, each with its
+  // chunks one after the other (8 rows of 128 bytes, swizzled), so that one
+  // TMA box brings whole keys.
+  static constexpr int kGroupBytes = CH * 1024;
   static constexpr int kSoftmaxWarps = 8 * NT;      // two threads a row
   static constexpr int kScoreWarp = kSoftmaxWarps, kValueWarp = kSoftmaxWarps + 1;
   static constexpr int kProducerWarp = kSoftmaxWarps + 2;  // and the query warp
   static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
   static constexpr int kSlotBytes = T * D * 2;      // one block of K or of V
   static constexpr int kSlots = 128 * 1024 / kSlotBytes;  // even: keys in the even slots, values in the odd ones
+  static_assert(kSlots % 2 == 0, "slots");
   static constexpr int kQBytes = kTileRows * D * 2;
   // Tensor memory: NS score buffers of T columns, two weight buffers of T / 2
   // (a column holds two weights of a row), then the tiles' accumulators.  At
@@ -343,10 +348,11 @@ __device__ bool producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *s
         }
         if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(nbox * bt * D * 2));
         __syncwarp();
-        for (int op0 = 0; op0 < nbox * C::CH; op0 += 32) {
-          const int op = op0 + lane, box = op / C::CH, ch = op % C::CH;
-          const int tok = tok0 + box * bt;
-          int pg = __shfl_sync(0xffffffffu, page, box & 31);
+        const void *map = kv ? (const void *)&tm.kv.v : (const void *)&tm.kv.k;
+        const int box = a.grouped ? lane : lane / C::CH, ch = a.grouped ? 0 : lane % C::CH;
+        for (int b0 = 0; b0 < nbox; b0 += a.grouped ? 32 : 32 / C::CH) {
+          const int tok = tok0 + (b0 + box) * bt;
+          int pg = __shfl_sync(0xffffffffu, page, (b0 + box) & 31);
           int row = s.b * a.page_size + tok;
           if (!a.contiguous) {
             // A box of hidden keys only is never read, whatever its table entry
@@ -354,14 +360,16 @@ __device__ bool producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *s
             // Both are placed at negative rows, which the map fills with zeros.
             const bool hidden = tok >= a.sinks && tok + bt <= span.low;
             if (hidden || pg < 0 || pg >= a.num_pages) {
-              bad_page |= !hidden && op < nbox * C::CH;
+              bad_page |= !hidden && b0 + box < nbox;
               pg = -1;
             }
             row = pg < 0 ? -a.page_size + tok % a.page_size : pg * a.page_size + tok % a.page_size;
           }
-          if (op < nbox * C::CH)
-            tma_load_3d(sbase + sl * C::kSlotBytes + ch * (T * 128) + box * bt * 128,
-                        kv ? (const void *)&tm.kv.v : (const void *)&tm.kv.k, ch * 64, s.h, row, full);
+          const uint32_t dst = sbase + sl * C::kSlotBytes + (b0 + box) * (bt / 8) * C::kGroupBytes + ch * 1024;
+          if (b0 + box < nbox) {
+            if (a.grouped) tma_load_4d(dst, map, 0, 0, s.h * C::CH, row >> 3, full);
+            else tma_load_3d(dst, map, ch * 64, s.h, row, full);
+          }
         }
         ++slot_n;
       }
@@ -475,7 +483,7 @@ template <int D, bool kBf16>
 __device__ bool issue_scores(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int lane) {
   using C = Cfg<D>;
   constexpr int T = C::T, NT = C::NT;
-  constexpr uint32_t kHi = smem_desc_hi(1024);
+  constexpr uint32_t kHi = smem_desc_hi(1024), kHiKV = smem_desc_hi(C::kGroupBytes);
   // a negative scale becomes positive with Q negated
   const uint32_t idesc = mma_idesc<kBf16>(kTileRows, T, false) | (a.scale_log2 < 0.f ? kIdescNegateA : 0u);
   const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
@@ -503,7 +511,7 @@ __device__ bool issue_scores(const PrefillArgs &a, uint8_t *smem, uint32_t tmem,
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss<kHi>(d, q + (kk / 4) * (kTileRows * 8) + (kk % 4) * 2, k + (kk / 4) * (T * 8) + (kk % 4) * 2, idesc, kk > 0);
+            mma_ss<kHi, kHiKV>(d, q + (kk / 4) * (kTileRows * 8) + (kk % 4) * 2, k + (kk / 4) * 64 + (kk % 4) * 2, idesc, kk > 0);
           mma_commit(bars + 8 * (C::B_SFULL + i));
           if (t + 1 == w.tiles) {
             mma_commit(bars + 8 * (C::B_EMPTY + slot));
@@ -528,7 +536,8 @@ template <int D, bool kBf16>
 __device__ bool issue_values(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int lane) {
   using C = Cfg<D>;
   constexpr int T = C::T, NT = C::NT;
-  constexpr uint32_t kHi = smem_desc_hi(1024);
+  constexpr uint32_t kHi = smem_desc_hi(C::kGroupBytes);
+  constexpr uint32_t kStep = 2 * C::kGroupBytes / 16;  // 16 keys
   constexpr uint32_t kIdesc = mma_idesc<kBf16>(kTileRows, D, true);
   const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
   int slot = 1, phase = 0;  // ring slot of the next values, and its phase
@@ -541,7 +550,7 @@ __device__ bool issue_values(const PrefillArgs &a, uint8_t *smem, uint32_t tmem,
     for (int j = 0; j < w.n; ++j) {
       const Steps st = steps_of<T>(a, w.span, w.span.block(w.beg + j) * T);
       if (!wait(C::B_FULL + slot, phase)) return false;
-      const uint32_t v = smem_desc_lo(sbase + slot * C::kSlotBytes, T * 128);
+      const uint32_t v = smem_desc_lo(sbase + slot * C::kSlotBytes, 1024);
       for (int t = 0; t < w.tiles; ++t) {
         const int i = NT == 2 ? t : (p_n[0] + p_n[1]) & 1;
         const uint32_t o = tmem + C::kOCol + t * D, p = tmem + C::kPCol + i * (T / 2);
@@ -550,9 +559,9 @@ __device__ bool issue_values(const PrefillArgs &a, uint8_t *smem, uint32_t tmem,
         if (elect_one()) {
           if (st.k0 == 0 && st.k1 == T / 16) {
 #pragma unroll
-            for (int kk = 0; kk < T / 16; ++kk) mma_ts<kHi>(o, p + kk * 8, v + kk * 128, kIdesc, kk > 0 || j > 0);
+            for (int kk = 0; kk < T / 16; ++kk) mma_ts<kHi>(o, p + kk * 8, v + kk * kStep, kIdesc, kk > 0 || j > 0);
           } else {
-            for (int kk = st.k0; kk < st.k1; ++kk) mma_ts<kHi>(o, p + kk * 8, v + kk * 128, kIdesc, kk > st.k0 || j > 0);
+            for (int kk = st.k0; kk < st.k1; ++kk) mma_ts<kHi>(o, p + kk * 8, v + kk * kStep, kIdesc, kk > st.k0 || j > 0);
           }
           mma_commit(bars + 8 * (C::B_OFULL + i));
           if (t + 1 == w.tiles) mma_commit(bars + 8 * (C::B_EMPTY + slot));
@@ -672,7 +681,7 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
           for (int i = st.k0 * 16 * (D / 8) + half * kTileRows + r; i < st.k1 * 16 * (D / 8); i += 2 * kTileRows) {
             const int key = i / (D / 8), c = i % (D / 8);
             if (key >= st.top || (key >= st.g0 && key < st.g1))
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + (c / 8) * (T * 128) + key * 128 + (c % 8) * 16),
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + (key / 8) * C::kGroupBytes + (c / 8) * 1024 + (key % 8) * 128 + (c % 8) * 16),
                            "r"(0u) : "memory");
           }
           fence_proxy_async_smem();  // before the product reads them
@@ -939,6 +948,54 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   }
 }
 
+// 4-D map {64 elements, 8 tokens, Hkv * D / 64 chunks, groups of 8 tokens} of a K
+// or V pool; box {64, 8, D / 64, box_tokens / 8}: whole keys of one head, in
+// the layout of a block in shared memory.  One box a page brings 2 to 4 times
+// fewer TMA operations than boxes of one chunk, which small pages are bound
+// by.
+bool encode_grouped_kv_map(CUtensorMap *m, const void *base, int D, int Hkv, long long pool_tokens, int box_tokens,
+                           bool bf16) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t token = (cuuint64_t)Hkv * D * 2;
+  cuuint64_t dims[4] = {64, 8, (cuuint64_t)Hkv * (D / 64), (cuuint64_t)(pool_tokens / 8)};
+  cuuint64_t strides[3] = {token, 128, 8 * token};
+  cuuint32_t box[4] = {64u, 8u, (cuuint32_t)(D / 64), (cuuint32_t)(box_tokens / 8)};
+  cuuint32_t estride[4] = {1u, 1u, 1u, 1u};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+             const_cast<void *>(base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B,
+             D >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The pair of maps, from a small per-thread cache (as kv_maps).
+bool grouped_kv_maps(TmapPair *tm, const void *k, const void *v, int D, int Hkv, long long pool_tokens, int box_tokens,
+                     bool bf16) {
+  struct Entry {
+    const void *k, *v;
+    long long pool_tokens;
+    int D, Hkv, box_tokens;
+    bool bf16, used;
+    TmapPair tm;
+  };
+  constexpr int kEntries = 4;
+  thread_local Entry cache[kEntries] = {};
+  thread_local int next = 0;
+  for (const Entry &e : cache)
+    if (e.used && e.k == k && e.v == v && e.pool_tokens == pool_tokens && e.D == D && e.Hkv == Hkv &&
+        e.box_tokens == box_tokens && e.bf16 == bf16) {
+      *tm = e.tm;
+      return true;
+    }
+  if (!encode_grouped_kv_map(&tm->k, k, D, Hkv, pool_tokens, box_tokens, bf16) ||
+      !encode_grouped_kv_map(&tm->v, v, D, Hkv, pool_tokens, box_tokens, bf16))
+    return false;
+  cache[next] = Entry{k, v, pool_tokens, D, Hkv, box_tokens, bf16, true, *tm};
+  next = (next + 1) % kEntries;
+  return true;
+}
+
 // 3-D map {D, Hq, tokens} of the packed queries; box {64, G, TQ}: one tile's
 // packed rows of one 64-column chunk, 128-byte swizzle.
 bool encode_q_map(CUtensorMap *m, const void *q, int D, int Hq, int total_q, int G, int TQ, bool bf16) {
@@ -971,15 +1028,18 @@ mxa_status_t launch_typed(const PrefillLaunch &L, PrefillArgs a, cudaStream_t st
     }
   }
   const mxa_decode_params_t &p = L.p;
-  // Boxes of whole 8-token groups of one page: the largest common divisor
-  // of the page and the block serves every page size that is a multiple of 8.
+  // Boxes of whole groups of 8 tokens of one page: the largest common divisor
+  // of the page and the block serves every page size that is a multiple of
+  // 8.  A contiguous cache whose rows do not start at multiples of 8 takes
+  // boxes of one group and one chunk.
   int box = C::T;
-  if (!a.contiguous)
-    while (p.page_size % box != 0) box /= 2;
+  a.grouped = p.page_size % 8 == 0;
+  while (box > 8 && (a.contiguous ? !a.grouped : p.page_size % box != 0)) box /= 2;
   a.box_tokens = box;
   PrefillMaps tm;
   const long long pool_tokens = (long long)(a.contiguous ? p.B : p.num_pages) * p.page_size;
-  if (!kv_maps(&tm.kv, L.k_cache, L.v_cache, D, p.Hkv, pool_tokens, box, kBf16) ||
+  if (!(a.grouped ? grouped_kv_maps(&tm.kv, L.k_cache, L.v_cache, D, p.Hkv, pool_tokens, box, kBf16)
+                  : kv_maps(&tm.kv, L.k_cache, L.v_cache, D, p.Hkv, pool_tokens, box, kBf16)) ||
       !encode_q_map(&tm.q, L.q, D, p.Hq, L.total_q, a.G, a.TQ, kBf16))
     return MXA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};

@@ -10,7 +10,7 @@
 namespace mxa {
 
 struct alignas(64) PrefillMaps {
-  TmapPair kv;     // the caches: boxes of {64 elements, 1 head, box_tokens tokens}
+  TmapPair kv;     // the caches: boxes of box_tokens keys of one head, or of one chunk of 8 of them
   CUtensorMap q;   // the packed queries: boxes of {64 elements, G heads, TQ tokens}
 };
 
@@ -34,6 +34,7 @@ struct PrefillArgs {
   int B, Hq, Hkv, G, TQ;       // TQ: tokens of a 128-row tile
   int total_q, max_q;
   int page_size, num_pages, mpps, contiguous, box_tokens;
+  int grouped;                 // boxes of whole keys (rows at multiples of 8 tokens), else of one chunk
   int max_seqlen_k;
   int causal, window, sinks;
   int unit_cost;               // fixed cost of a unit, in KV blocks

@@ -85,13 +85,13 @@ __host__ __device__ constexpr uint32_t mma_idesc(int M, int N, bool transpose_b)
 constexpr uint32_t kIdescNegateA = 1u << 13;
 
 // D += A B (or D = A B), A and B in shared memory; issued by one thread.
-template <uint32_t kHi>
+template <uint32_t kHiA, uint32_t kHiB = kHiA>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kHi)
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kHiA), "n"(kHiB)
       : "memory");
 }
 // A in tensor memory (a column holds two consecutive 16-bit values of a row).

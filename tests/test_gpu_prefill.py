@@ -67,7 +67,7 @@ LENGTHS = [700, 50, 33, 1000, 129, 3, 1025]  # the sixth row has more queries th
 
 
 @pytest.mark.parametrize("D,dtype,page_size", [(128, "bf16", 16), (64, "f16", 8), (256, "bf16", 64), (128, "f16", 0),
-                                               (64, "bf16", 24), (256, "f16", 128), (128, "bf16", 192)])
+                                               (64, "bf16", 24), (256, "f16", 128), (128, "bf16", 192), (64, "f16", 0)])
 @pytest.mark.parametrize("causal,window,sinks", [(True, 0, 0), (False, 0, 0), (True, 1, 0), (True, 100, 4),
                                                  (True, 257, 130), (True, 64, 64), (True, 5000, 9)])
 def test_matches_oracle(D, dtype, page_size, causal, window, sinks):
