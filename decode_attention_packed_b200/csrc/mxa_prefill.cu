@@ -296,10 +296,6 @@ __device__ bool producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *s
   constexpr int T = C::T;
   const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
   Segment *descs = reinterpret_cast<Segment *>(smem + C::kDescOff);
-  if (lane == 0) {
-    prefetch_tmap(&tm.kv.k);
-    prefetch_tmap(&tm.kv.v);
-  }
   Walk w = walk_start<D>(a, reinterpret_cast<int *>(smem), lane);
   fence_proxy_async_smem();  // the scan's accesses precede the ring's loads
   __syncwarp();
@@ -395,7 +391,6 @@ __device__ bool queries(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *sm
   constexpr int NT = C::NT;
   const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
   const Segment *descs = reinterpret_cast<const Segment *>(smem + C::kDescOff);
-  if (lane == 0) prefetch_tmap(&tm.q);
   int seg_n = 0;
   bool ok = true;
   for (;; ++seg_n) {
@@ -624,31 +619,38 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
   for (;;) {
     const int d = seg_n % kDescs;
     if (!wait(C::B_DFULL + d, seg_n / kDescs)) return false;
-    const Segment s = descs[d];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bars + 8 * (C::B_DEMPTY + d));
-    ++seg_n;
-    if (s.kind < 0) return true;
+    // The slot is kept until the unit is done: what the loop over the blocks
+    // does not need is read again from it, not held in registers.
+    const volatile Segment &s = descs[d];
+    auto done = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (C::B_DEMPTY + d));
+      ++seg_n;
+    };
+    if (s.kind < 0) {
+      done();
+      return true;
+    }
+    const int blk_beg = s.beg, blk_end = s.end, L = s.L, qn = s.qn;
     const int u0 = s.it * NT * a.TQ, tt0 = u0 + t * a.TQ;  // first token of the unit and of this tile
-    if (tt0 >= s.qn) {                                      // the unit's second tile is empty
-      slot_n += 2 * (s.end - s.beg);
+    if (tt0 >= qn) {                                        // the unit's second tile is empty
+      slot_n += 2 * (blk_end - blk_beg);
+      done();
       continue;
     }
-    const Span span = span_of<T>(a, s.L, s.qn, u0, min(u0 + NT * a.TQ, s.qn));
-    const int tok = tt0 + r_tok;
-    const bool real = r_tok < a.TQ && tok < s.qn;
+    const Span span = span_of<T>(a, L, qn, u0, min(u0 + NT * a.TQ, qn));
     // keys this row sees: [0, sinks) and [low, lim)
-    int lim = a.causal ? min(s.L, s.L - s.qn + tok + 1) : s.L;
-    if (!real) lim = 0;
+    int lim = a.causal ? min(L, L - qn + tt0 + r_tok + 1) : L;
+    if (r_tok >= a.TQ || tt0 + r_tok >= qn) lim = 0;
     const int low = a.window > 0 ? max(lim - a.window, 0) : 0;
     // a block lies at an edge unless every row of the tile sees all of it;
     // one whose values need clearing always does: its hidden keys lie past
     // every row's, or before every row's window
-    const int tile_lim = a.causal ? s.L - s.qn + tt0 + 1 : s.L;
-    const int tile_low = a.window > 0 ? s.L - s.qn + min(tt0 + a.TQ, s.qn) - a.window : 0;
+    const int tile_lim = a.causal ? L - qn + tt0 + 1 : L;
+    const int tile_low = a.window > 0 ? L - qn + min(tt0 + a.TQ, qn) - a.window : 0;
 
     float m = -INFINITY, l = 0.f;  // running maximum (base 2, scaled) and sum
-    for (int blk = s.beg; blk < s.end; ++blk) {
+    for (int blk = blk_beg; blk < blk_end; ++blk) {
       // barriers: the tile's, or with one tile those of the block's parity
       const int u = NT == 2 ? t : blk_n & 1, un = NT == 2 ? blk_n : blk_n >> 1;
       if (!wait(C::B_SFULL + u, un)) return false;
@@ -664,15 +666,18 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
       if (lane == 0) mbar_arrive(bars + 8 * (C::B_SFREE + u));
       const int j0 = span.block(blk) * T;
       if (j0 + T > tile_lim || (j0 < tile_low && j0 + T > a.sinks)) {
-        // one bit a key: seen or not
+        // one bit a key: seen or not; most groups of 32 are seen whole
 #pragma unroll
         for (int c = 0; c < TH; c += 32) {
           const int j = j0 + half * TH + c;
           const uint32_t seen = bits_below(lim - j) & (~bits_below(low - j) | bits_below(a.sinks - j));
+          if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[c + i] = (seen >> i) & 1u ? x[c + i] : -INFINITY;
+            for (int i = 0; i < 32; ++i) x[c + i] = (seen >> i) & 1u ? x[c + i] : -INFINITY;
+          }
         }
-        const Steps st = steps_of<T>(a, span, j0);
+        const int b0 = s.it * NT * a.TQ;
+        const Steps st = steps_of<T>(a, span_of<T>(a, s.L, s.qn, b0, min(b0 + NT * a.TQ, (int)s.qn)), j0);
         if (t == 0 && st.clear) {  // values of hidden keys become zeros
           const int sl = slot_n % C::kSlots;
           if (!wait(C::B_FULL + sl, slot_n / C::kSlots)) return false;
@@ -704,7 +709,7 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
         const float alpha = m == mn ? 1.f : ex2(m - mn);
         m = mn;
         l *= alpha;
-        if (blk > s.beg) {
+        if (blk > blk_beg) {
           // the values of the block before are in the accumulator
           const int pu = NT == 2 ? t : u ^ 1, pn = NT == 2 ? un - 1 : (blk_n - 2) >> 1;
           if (!wait(C::B_OFULL + pu, pn)) return false;
@@ -755,7 +760,8 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     // and once more, before the rows overwrite the place of the sums
     if (!exchange(0.f, l_other)) return false;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int hq = s.h * a.G + r_head;
+    const int hq = s.h * a.G + r_head, v0 = s.it * NT * a.TQ, tok = v0 + t * a.TQ + r_tok;
+    const bool real = r_tok < a.TQ && tok < s.qn;
     // Where the row goes: row `row` of the output, or of the CTA's piece slot.
     const int row0 = s.kind == 0 ? (s.q0 + tok) * a.Hq + hq
                                  : (blockIdx.x * 2 + (s.kind - 1)) * (NT * kTileRows) + t * kTileRows + r;
@@ -770,8 +776,8 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
       PieceDesc &pd = a.pieces[blockIdx.x];
       pd.q0 = s.q0;
       pd.h = s.h;
-      pd.t0 = u0;
-      pd.tokens = min(NT * a.TQ, s.qn - u0);
+      pd.t0 = v0;
+      pd.tokens = min(NT * a.TQ, s.qn - v0);
       pd.c_first = s.c_first;
       pd.n_pieces = s.n_pieces;
     }
@@ -807,14 +813,19 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
                          pack2<kBf16>(o[8 * i + 4], o[8 * i + 5]), pack2<kBf16>(o[8 * i + 6], o[8 * i + 7]));
       }
       __syncwarp();
-#pragma unroll 1
-      for (int rr = lane >> shift; rr < 32; rr += 32 >> shift) {
-        const int to = __shfl_sync(0xffffffffu, row, rr);
-        const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
-        if (to >= 0) *reinterpret_cast<uint4 *>(dst + (((size_t)to * D + col) << shift) + c * 16) = v;
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {  // two rows in flight (16-bit rows are done after two)
+        if (k > 0 && !piece) break;
+        const int ra = (lane >> shift) + k * (32 >> shift), rb = ra + (32 >> shift);
+        const int ta = __shfl_sync(0xffffffffu, row, ra), tb = __shfl_sync(0xffffffffu, row, rb);
+        const uint4 va = *reinterpret_cast<const uint4 *>(stage + ra * 64 + ((c ^ ((ra >> 1) & 3)) << 4));
+        const uint4 vb = *reinterpret_cast<const uint4 *>(stage + rb * 64 + ((c ^ ((rb >> 1) & 3)) << 4));
+        if (ta >= 0) *reinterpret_cast<uint4 *>(dst + (((size_t)ta * D + col) << shift) + c * 16) = va;
+        if (tb >= 0) *reinterpret_cast<uint4 *>(dst + (((size_t)tb * D + col) << shift) + c * 16) = vb;
       }
     }
     tc_fence_before();  // the accumulator has been read before this thread's next arrival
+    done();
   }
 }
 
@@ -851,6 +862,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     fence_mbar_init();
   }
   if (warp == C::kScoreWarp) tmem_alloc(tmem_slot, 512);
+  if (tid == 32 * C::kProducerWarp) {
+    prefetch_tmap(&tm.kv.k);
+    prefetch_tmap(&tm.kv.v);
+    prefetch_tmap(&tm.q);
+  }
   grid_launch_dependents();
   // Inputs may be written, and outputs and workspace used, by the kernel
   // this launch depends on.

@@ -121,14 +121,21 @@ def _check(code: int, where: str) -> None:
         raise MxaError(code, where)
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+# The current stream's handle without a Stream object around it, which costs
+# more host time than the rest of a short call's marshalling.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 # --------------------------------------------------------------------------
@@ -465,38 +472,36 @@ def prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, ma
                                    max_seqlen_k=max_seqlen_k)
         if stream is not None and not isinstance(stream, int):
             prepared.workspace.record_stream(stream)
-    _want(q, "q", q.dtype)
-    _want(k_cache, "k_cache", q.dtype)
-    _want(v_cache, "v_cache", q.dtype, k_cache.shape)
-    _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, (prepared.params.B + 1,))
-    _want(cache_seqlens, "cache_seqlens", torch.int32, (prepared.params.B,))
+    dev, dtype, B = torch.cuda.current_device(), q.dtype, prepared.params.B
+    _want(dev, q, "q", dtype)
+    _want(dev, k_cache, "k_cache", dtype)
+    _want(dev, v_cache, "v_cache", dtype, k_cache.shape)
+    _want(dev, cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
+    _want(dev, cache_seqlens, "cache_seqlens", torch.int32, (B,))
     if block_table is not None:
-        _want(block_table, "block_table", torch.int32, (prepared.params.B, prepared.params.max_pages_per_seq))
+        _want(dev, block_table, "block_table", torch.int32, (B, prepared.params.max_pages_per_seq))
     if out is None:
         out = torch.empty_like(q)
     else:
-        _want(out, "out", q.dtype, q.shape)
+        _want(dev, out, "out", dtype, q.shape)
     if lse is None and return_lse:
         lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
     elif lse is not None:
-        _want(lse, "lse", torch.float32, (q.shape[1], q.shape[0]))
+        _want(dev, lse, "lse", torch.float32, (q.shape[1], q.shape[0]))
     mxa_prefill_fwd(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, prepared.params, scale, causal,
                     window, sinks, prepared.workspace, out, lse, stream)
     return out, lse
 
 
-def _want_here(t: torch.Tensor, name: str) -> None:
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device")
-
-
-def _want(t: torch.Tensor, name: str, dtype, shape=None) -> None:
-    """A dense tensor of `dtype` (and `shape`) on the current device, or an error that names it."""
+def _want(device: int, t: torch.Tensor, name: str, dtype, shape=None) -> None:
+    """A dense tensor of `dtype` (and `shape`) on CUDA device `device`, the
+    current one, or an error that names it."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    _want_here(t, name)
+    if t.get_device() != device:  # -1 for a tensor on the host
+        raise ValueError(f"{name} must be on the current CUDA device")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
 
@@ -512,21 +517,24 @@ def extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, *, page_
     Returns (slots [total_q], new_seqlens [B], pages_used [1]), int32.  A row
     whose pages do not fit its table or the free list takes none: its slots
     are -1 and its length is unchanged."""
-    _want(block_table, "block_table", torch.int32)
+    dev, int32 = torch.cuda.current_device(), torch.int32
+    _want(dev, block_table, "block_table", int32)
     B = block_table.shape[0]
-    dev = block_table.device
-    _want(cache_seqlens, "cache_seqlens", torch.int32, (B,))
-    _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
-    _want(free_pages, "free_pages", torch.int32)
+    _want(dev, cache_seqlens, "cache_seqlens", int32, (B,))
+    _want(dev, cu_seqlens_q, "cu_seqlens_q", int32, (B + 1,))
+    _want(dev, free_pages, "free_pages", int32)
     if slots is None:
-        slots = torch.empty(total_q, dtype=torch.int32, device=dev)
+        slots = torch.empty(total_q, dtype=int32, device=block_table.device)
+    else:
+        _want(dev, slots, "slots", int32, (total_q,))
     if new_seqlens is None:
-        new_seqlens = torch.empty(B, dtype=torch.int32, device=dev)
+        new_seqlens = torch.empty_like(cache_seqlens)
+    else:
+        _want(dev, new_seqlens, "new_seqlens", int32, (B,))
     if pages_used is None:
-        pages_used = torch.empty(1, dtype=torch.int32, device=dev)
-    _want(slots, "slots", torch.int32, (total_q,))
-    _want(new_seqlens, "new_seqlens", torch.int32, (B,))
-    _want(pages_used, "pages_used", torch.int32, (1,))
+        pages_used = torch.empty(1, dtype=int32, device=block_table.device)
+    else:
+        _want(dev, pages_used, "pages_used", int32, (1,))
     if B and new_seqlens.data_ptr() == cache_seqlens.data_ptr():
         raise ValueError("new_seqlens must be another buffer than cache_seqlens")
     mxa_extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, page_size, num_pages, slots,
@@ -538,18 +546,20 @@ def write_cache(k_new, v_new, k_cache, v_cache, slots, *, stream=None) -> None:
     """Copy k_new / v_new [total, Hkv, D] into the cache slots of
     extend_tables.  The tokens may be strided (slices of one fused
     projection); a token with slot -1 is left out; slots are distinct."""
-    _want(k_cache, "k_cache", k_cache.dtype)
-    _want(v_cache, "v_cache", k_cache.dtype, k_cache.shape)
-    if k_cache.dtype is not torch.bfloat16 and k_cache.dtype is not torch.float16:
+    dev, dtype = torch.cuda.current_device(), k_cache.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise TypeError("the cache must be float16 or bfloat16")
+    _want(dev, k_cache, "k_cache", dtype)
+    _want(dev, v_cache, "v_cache", dtype, k_cache.shape)
     total, Hkv, D = k_new.shape
     for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if t.dtype is not k_cache.dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"{name} must have the cache's type")
-        _want_here(t, name)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the current CUDA device")
         if t.shape != (total,) + k_cache.shape[2:]:
             raise ValueError(f"{name} must be [total, Hkv, D] with the cache's heads")
         if total and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != D)):
             raise ValueError(f"a token of {name} must be contiguous")
-    _want(slots, "slots", torch.int32, (total,))
+    _want(dev, slots, "slots", torch.int32, (total,))
     mxa_cache_write(k_new, v_new, slots, k_cache, v_cache, stream)
