@@ -22,8 +22,8 @@ def test_window_plan_is_sized_by_the_keys_a_window_leaves():
     p = params(B=1, Hq=8)
     full, windowed = mxa.mxa_plan(p, 0, sm_count=148), mxa.mxa_plan_window(p, 512, 4, sm_count=148)
     # 8 units of 256 blocks fill the wave; a window of 512 keys leaves
-    # (512 + 0 + 4 + 3 * 64) / 64 = 12 blocks (rounded up), pieces of 4
-    assert full.grid == 296 and windowed.grid == 8 * (12 + 3) // 4
+    # (512 + 0 + 4 + 3 * 64) / 64 = 12 blocks (rounded up), pieces of 2
+    assert full.grid == 296 and windowed.grid == 8 * 12 // 2
     # a window as long as the rows plans like none
     assert mxa.mxa_plan_window(p, 16384, 0, sm_count=148).as_dict() == full.as_dict()
     assert mxa.mxa_plan_window(p, 2**31 - 1, 2**31 - 1, sm_count=148).as_dict() == full.as_dict()
