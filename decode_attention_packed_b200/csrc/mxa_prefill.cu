@@ -3,7 +3,7 @@
 //
 //   O = softmax(scale Q K^T + mask) V,   LSE = ln sum_j exp(scale q . k_j)
 //
-// Each CTA walks a contiguous share of the work with three roles:
+// Each CTA walks a contiguous share of the work with these roles:
 //  - a producer warp finds the CTA's share, gathers K and V pages through the
 //    block table with TMA into a ring of shared-memory slots; a query warp
 //    loads the packed query rows;
@@ -25,6 +25,18 @@
 // batches, causal triangles and single long rows all give every CTA the same
 // work.  A unit cut by a range's end leaves float32 pieces with their LSEs in
 // the workspace, which a second small kernel merges.
+//
+// What bounds it (B200, per pair of tiles and 128 keys).  D = 128: the tensor
+// cores 2048 cycles (four products of 512), the exponentials 2048 (16 a cycle
+// and SM, both tiles' 32768).  D = 64: 1024 and 2048.  Measured: about 3000 to
+// 3100 in either case, since a tile's loads, maximum, hand-overs and stores are
+// only partly hidden behind the other tile's exponentials; 4096 tokens after
+// 12288 keys (64 query heads, 8 KV heads, D = 128) run at 1260 TFLOP/s for a
+// millisecond or two and at about 1050 when the card's power limit holds the
+// clock.  Tried and not kept: computing part of the exponentials with a
+// polynomial on the floating-point pipe (an eighth: no change; a quarter:
+// slower), turns of the two tiles at the exponentials (no change), handing the
+// weights over in two parts (slower), a fifth ring slot (no change).
 #include "mxa_config.h"
 #include "mxa_device.cuh"
 #include "mxa_launch.h"
@@ -53,8 +65,8 @@ struct Cfg {
   static constexpr int kProducerWarp = kSoftmaxWarps + 2;  // and the query warp
   static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
   static constexpr int kSlotBytes = T * D * 2;      // one block of K or of V
-  static constexpr int kSlots = 128 * 1024 / kSlotBytes;  // even: keys in the even slots, values in the odd ones
-  static_assert(kSlots % 2 == 0, "slots");
+  static constexpr int kSlots = 128 * 1024 / kSlotBytes;
+  static_assert(kSlots % 2 == 0, "keys in the even slots, values in the odd ones");
   static constexpr int kQBytes = kTileRows * D * 2;
   // Tensor memory: NS score buffers of T columns, two weight buffers of T / 2
   // (a column holds two weights of a row), then the tiles' accumulators.  At
@@ -912,8 +924,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 // Merge of the units that ranges cut: cut i (between CTAs i - 1 and i) of a
 // unit with n pieces takes the (i - c_first)-th share of its rows, and
 // blockIdx.y a part of that: two rows a warp where a unit has two pieces, since
-// a row is a chain of a few dependent loads.  LSE = ln sum exp(lse_p), O = sum exp(lse_p - LSE) O_p.
-// One warp a row.
+// a row is a chain of a few dependent loads (with a quarter of the warps the
+// merge took 20 us of a 240 us call, now under 5).
+//   LSE = ln sum_p exp(lse_p),   O = sum_p exp(lse_p - LSE) O_p
 // ---------------------------------------------------------------------------
 constexpr int kMergeThreads = 256, kMergeParts = 16;
 template <int D, bool kBf16>
@@ -945,7 +958,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
       for (int p = lane; p < n; p += 32) sum += ex2(a.lse_part[slot_of(p) * (NT * kTileRows) + row] * kLog2e - mx);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float lse2 = sum > 0.f ? mx + log2f(sum) : -INFINITY;
+    const float lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum);  // NaN stays
     const int hq = pd.h * a.G + g, token = pd.q0 + pd.t0 + tok;
     if (lane == 0 && a.lse != nullptr) a.lse[(size_t)hq * a.total_q + token] = lse2 * kLn2;
     for (int c = lane * 4; c < D; c += 128) {

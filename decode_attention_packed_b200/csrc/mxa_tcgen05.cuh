@@ -41,16 +41,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14,"
-      " %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14,"
@@ -132,36 +122,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
-}
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
-// 2^x on the floating-point pipe, for x < 100, to relieve the special-function
-// unit: x = n + f with n the nearest integer (added to and taken from 1.5 *
-// 2^23, where a float's last bit is one: Cody and Waite's reduction), 2^f by a
-// polynomial of degree 4 (least maximal relative error over [-1/2, 1/2],
-// fitted by Lawson's algorithm: 2.7e-6), times 2^n, whose exponent bits are
-// the sum's last ones.  x below -126 gives 2^-126 instead of less; NaN stays.
-__device__ __forceinline__ float2 ex2_poly(float2 x) {
-  constexpr float kShift = 12582912.f + 127.f;
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-126.f));
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-126.f));
-  const float2 t = add2(x, make_float2(kShift, kShift));
-  const float2 n = add2(t, make_float2(-kShift, -kShift));
-  const float2 f = fma2(n, make_float2(-1.f, -1.f), x);
-  auto c = [](float v) { return make_float2(v, v); };
-  float2 p = fma2(c(0.009570102207362652f), f, c(0.05591785907745361f));
-  p = fma2(p, f, c(0.240247443318367f));
-  p = fma2(p, f, c(0.6931217908859253f));
-  p = fma2(p, f, c(0.9999992847442627f));
-  return mul2(p, make_float2(__uint_as_float(__float_as_uint(t.x) << 23), __uint_as_float(__float_as_uint(t.y) << 23)));
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {

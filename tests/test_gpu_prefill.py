@@ -93,6 +93,15 @@ def test_small_and_single(q_lens, lengths, D):
         check(inp, q, cu, *run(inp, q, cu, causal=causal), causal)
 
 
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "f16"), (256, "bf16")])
+@pytest.mark.parametrize("longest", [1024, 1029])
+def test_contiguous_rows_at_any_place(D, dtype, longest):
+    # the rows of a contiguous cache start at multiples of 8 tokens, or not
+    inp, q, cu = draw([130, 1, 40], [700, 200, longest], D=D, dtype=dtype, page_size=0, seed=1250)
+    for window, sinks in ((0, 0), (150, 9)):
+        check(inp, q, cu, *run(inp, q, cu, window=window, sinks=sinks), True, window, sinks)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_peaked_scores_rescale_the_accumulator(D):
     # keys times 12, and rising along the row: the running maximum grows many times
