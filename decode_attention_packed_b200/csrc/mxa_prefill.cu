@@ -771,7 +771,7 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     l = half == 0 ? l + l_other : l_other + l;  // the same sum in both halves
     // and once more, before the rows overwrite the place of the sums
     if (!exchange(0.f, l_other)) return false;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = l == 0.f ? 0.f : rcp(l);
     const int hq = s.h * a.G + r_head, v0 = s.it * NT * a.TQ, tok = v0 + t * a.TQ + r_tok;
     const bool real = r_tok < a.TQ && tok < s.qn;
     // Where the row goes: row `row` of the output, or of the CTA's piece slot.
@@ -779,7 +779,7 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
                                  : (blockIdx.x * 2 + (s.kind - 1)) * (NT * kTileRows) + t * kTileRows + r;
     const int row = real ? row0 : -1;
     if (real && half == 0) {
-      const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      const float lse = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
       if (s.kind != 0) a.lse_part[row0] = lse;
       else if (a.lse != nullptr) a.lse[(size_t)hq * a.total_q + s.q0 + tok] = lse;
     }
