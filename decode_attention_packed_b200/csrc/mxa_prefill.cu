@@ -157,10 +157,21 @@ __device__ __forceinline__ Span walk_span(const PrefillArgs &a, const Walk &w) {
   return span_of<Cfg<D>::T>(a, w.L, w.qn, t0, min(t0 + NT * a.TQ, w.qn));
 }
 
+// The first row from b on that has queries (a.B: none), 32 rows at a time; one warp.
+__device__ __forceinline__ int next_row(const PrefillArgs &a, int b, int lane) {
+  for (; b < a.B; b += 32) {
+    int q0, qn = 0, L;
+    if (b + lane < a.B) row_of(a, b + lane, q0, qn, L);
+    const unsigned some = __ballot_sync(0xffffffffu, qn > 0);
+    if (some != 0) return b + __ffs(some) - 1;
+  }
+  return a.B;
+}
+
 // The segment at the walk, which moves past it and past the fixed cost of
-// the unit that follows.
+// the unit that follows; one warp.
 template <int D>
-__device__ Segment walk_take(const PrefillArgs &a, Walk &w) {
+__device__ Segment walk_take(const PrefillArgs &a, Walk &w, int lane) {
   Segment s;
   const int len = min(w.nb - w.blk, w.end - w.x);
   s.b = w.b; s.h = w.h; s.it = w.it;
@@ -179,13 +190,12 @@ __device__ Segment walk_take(const PrefillArgs &a, Walk &w) {
       w.it = 0;
       if (++w.h == a.Hkv) {
         w.h = 0;
-        do {
-          if (++w.b == a.B) {
-            w.x = w.end;
-            return s;
-          }
-          row_of(a, w.b, w.q0, w.qn, w.L);
-        } while (w.qn == 0);
+        w.b = next_row(a, w.b + 1, lane);
+        if (w.b == a.B) {
+          w.x = w.end;
+          return s;
+        }
+        row_of(a, w.b, w.q0, w.qn, w.L);
         w.tiles = (w.qn + Cfg<D>::NT * a.TQ - 1) / (Cfg<D>::NT * a.TQ);
       }
     }
@@ -195,19 +205,33 @@ __device__ Segment walk_take(const PrefillArgs &a, Walk &w) {
   return s;
 }
 
-// Positions of one KV head's units of a row, over the lanes of a warp.
+// Positions of the groups of tiles first, first + step, ... of a row's units
+// of one KV head.
 template <int D>
-__device__ __forceinline__ int row_positions(const PrefillArgs &a, int qn, int L, int lane) {
-  constexpr int NT = Cfg<D>::NT;
-  const int tiles = (qn + NT * a.TQ - 1) / (NT * a.TQ);
+__device__ __forceinline__ int positions_of(const PrefillArgs &a, int qn, int L, int first, int step) {
+  const int tokens = Cfg<D>::NT * a.TQ;
   int sum = 0;
-  for (int it = lane; it < tiles; it += 32) {
-    const int t0 = it * NT * a.TQ;
-    sum += a.unit_cost + span_of<Cfg<D>::T>(a, L, qn, t0, min(t0 + NT * a.TQ, qn)).nb;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  for (int t0 = first * tokens; t0 < qn; t0 += step * tokens)
+    sum += a.unit_cost + span_of<Cfg<D>::T>(a, L, qn, t0, min(t0 + tokens, qn)).nb;
   return sum;
+}
+
+// Positions of each of 32 rows, b + lane, of one KV head; one warp.  A lane
+// counts its own row, and the warp together the rows of many groups.
+template <int D>
+__device__ __forceinline__ int row_positions(const PrefillArgs &a, int b, int lane) {
+  int q0, qn = 0, L = 0;
+  if (b + lane < a.B) row_of(a, b + lane, q0, qn, L);
+  const bool many = qn > 8 * Cfg<D>::NT * a.TQ;
+  int n = many ? 0 : positions_of<D>(a, qn, L, 0, 1);
+  for (unsigned left = __ballot_sync(0xffffffffu, many); left != 0; left &= left - 1) {
+    const int r = __ffs(left) - 1;
+    int sum = positions_of<D>(a, __shfl_sync(0xffffffffu, qn, r), __shfl_sync(0xffffffffu, L, r), lane, 32);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == r) n = sum;
+  }
+  return n;
 }
 
 // This CTA's range, from the rows' positions (`rows`, of one KV head each, in
@@ -223,7 +247,7 @@ __device__ Walk walk_start(const PrefillArgs &a, int *rows, int lane) {
   const int lo = min(lane * chunk, a.B), hi = min(lo + chunk, a.B);
   int sum = 0;
   for (int i = lo; i < hi; ++i) sum += rows[i];
-  int incl = sum;
+  long long incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -323,7 +347,7 @@ __device__ bool producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *s
     const bool more = w.x < w.end;
     const Walk at = w;
     Segment s;
-    if (more) s = walk_take<D>(a, w);
+    if (more) s = walk_take<D>(a, w, lane);
     else s.kind = -1;
     const int d = seg_n % kDescs;
     if (!wait_phase(bars + 8 * (C::B_DEMPTY + d), ((seg_n / kDescs) & 1) ^ 1)) {
@@ -885,13 +909,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   grid_dependency_wait();
   // the rows' positions, for the producer's scan (the ring is still unused)
   int *rows = reinterpret_cast<int *>(smem);
-  for (int b = warp; b < a.B; b += C::kThreads / 32) {
-    int q0, qn, L;
-    row_of(a, b, q0, qn, L);
-    const int n = row_positions<D>(a, qn, L, lane);
-    if (lane == 0) {
-      rows[b] = n;
-      if (b % (int)gridDim.x == (int)blockIdx.x) check_row(a, b);
+  for (int b = warp * 32; b < a.B; b += C::kThreads) {
+    const int n = row_positions<D>(a, b, lane);
+    if (b + lane < a.B) {
+      rows[b + lane] = n;
+      if ((b + lane) % (int)gridDim.x == (int)blockIdx.x) check_row(a, b + lane);
     }
   }
   if (tid == 0) a.pieces[blockIdx.x].n_pieces = 0;  // until a head piece says otherwise

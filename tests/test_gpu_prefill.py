@@ -246,3 +246,19 @@ def test_no_queries_and_refusals():
         mxa.prefill(qd, cd[:2], *args, max_seqlen_q=4, prepared=mxa.prepare_prefill(qd, cd, args[0], args[2], max_seqlen_q=4))
     with pytest.raises(TypeError):
         mxa.prefill(qd, cd, args[0].half(), *args[1:], max_seqlen_q=4)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_most_of_them_idle(D):
+    # thousands of rows; long runs without queries, single tokens, one long chunk
+    B = 3000
+    q_lens = [0] * B
+    for b in (0, 7, 700, 701, 702, 1999, 2998):
+        q_lens[b] = 1 + b % 3
+    q_lens[1500] = 900
+    lengths = [5] * B
+    for b in range(B):
+        if q_lens[b]:
+            lengths[b] = q_lens[b] + b % 50
+    inp, q, cu = draw(q_lens, lengths, Hq=2, Hkv=1, D=D, seed=1650)
+    check(inp, q, cu, *run(inp, q, cu))
