@@ -131,7 +131,7 @@ mxa_status_t check_prefill(const mxa_decode_params_t *p, int total_q) {
   if (p->D != 64 && p->D != 128 && p->D != 256) return MXA_ERR_UNSUPPORTED;
   if (p->Hq / p->Hkv > 128 || p->B > kMaxBalancedRows) return MXA_ERR_UNSUPPORTED;
   if ((long long)p->num_pages * p->page_size > INT32_MAX) return MXA_ERR_UNSUPPORTED;  // TMA coordinates
-  if ((long long)total_q + p->max_seqlen_k > INT32_MAX) return MXA_ERR_UNSUPPORTED;    // positions
+  if ((long long)total_q + p->max_seqlen_k > INT32_MAX / 2) return MXA_ERR_UNSUPPORTED;  // positions
   if ((long long)total_q * p->Hq > INT32_MAX) return MXA_ERR_UNSUPPORTED;              // output rows
   if (prefill_positions(*p, total_q) > INT32_MAX / 2) return MXA_ERR_UNSUPPORTED;      // the laid-out work
   return MXA_OK;

@@ -137,7 +137,7 @@ __device__ __forceinline__ void check_row(const PrefillArgs &a, int b) {
   const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1], l = a.seqlens[b];
   int bad = 0;
   if (l < 0 || l > a.max_seqlen_k) bad |= kErrBadLen;
-  if (c1 < c0 || (long long)c1 - c0 > a.max_q || (b == 0 && c0 != 0) || (b == a.B - 1 && c1 != a.total_q))
+  if (c1 < c0 || (long long)c1 - c0 > a.max_q || (b == 0 && c0 != 0) || c1 > a.total_q)
     bad |= kErrBadOffsets;
   if (bad) atomicOr(a.err, bad);
 }
@@ -245,22 +245,25 @@ __device__ Walk walk_start(const PrefillArgs &a, int *rows, int lane) {
   w.per_cta = 1;
   const int chunk = (a.B + 31) / 32;
   const int lo = min(lane * chunk, a.B), hi = min(lo + chunk, a.B);
-  int sum = 0;
+  long long sum = 0;
   for (int i = lo; i < hi; ++i) sum += rows[i];
   long long incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  const int total = __shfl_sync(0xffffffffu, incl, 31) * a.Hkv;
-  int run = incl - sum;
+  const long long all = __shfl_sync(0xffffffffu, incl, 31) * a.Hkv;
+  // More than total_q tokens can make: rows overlap (check_row has reported
+  // their offsets), and nothing is run.  Below the bound 32 bits are enough.
+  if (all == 0 || all > a.max_positions) return w;
+  const int total = (int)all;
+  int run = (int)(incl - sum);
   for (int i = lo; i < hi; ++i) {
     run += rows[i];
     rows[i] = run;
   }
   __syncwarp();
-  if (total == 0) return w;
   w.per_cta = (total + (int)gridDim.x - 1) / (int)gridDim.x;
   const int x0 = blockIdx.x * w.per_cta;
   if (x0 >= total) return w;
@@ -1020,33 +1023,6 @@ bool encode_grouped_kv_map(CUtensorMap *m, const void *base, int D, int Hkv, lon
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The pair of maps, from a small per-thread cache (as kv_maps).
-bool grouped_kv_maps(TmapPair *tm, const void *k, const void *v, int D, int Hkv, long long pool_tokens, int box_tokens,
-                     bool bf16) {
-  struct Entry {
-    const void *k, *v;
-    long long pool_tokens;
-    int D, Hkv, box_tokens;
-    bool bf16, used;
-    TmapPair tm;
-  };
-  constexpr int kEntries = 4;
-  thread_local Entry cache[kEntries] = {};
-  thread_local int next = 0;
-  for (const Entry &e : cache)
-    if (e.used && e.k == k && e.v == v && e.pool_tokens == pool_tokens && e.D == D && e.Hkv == Hkv &&
-        e.box_tokens == box_tokens && e.bf16 == bf16) {
-      *tm = e.tm;
-      return true;
-    }
-  if (!encode_grouped_kv_map(&tm->k, k, D, Hkv, pool_tokens, box_tokens, bf16) ||
-      !encode_grouped_kv_map(&tm->v, v, D, Hkv, pool_tokens, box_tokens, bf16))
-    return false;
-  cache[next] = Entry{k, v, pool_tokens, D, Hkv, box_tokens, bf16, true, *tm};
-  next = (next + 1) % kEntries;
-  return true;
-}
-
 // 3-D map {D, Hq, tokens} of the packed queries; box {64, G, TQ}: one tile's
 // packed rows of one 64-column chunk, 128-byte swizzle.
 bool encode_q_map(CUtensorMap *m, const void *q, int D, int Hq, int total_q, int G, int TQ, bool bf16) {
@@ -1089,8 +1065,9 @@ mxa_status_t launch_typed(const PrefillLaunch &L, PrefillArgs a, cudaStream_t st
   a.box_tokens = box;
   PrefillMaps tm;
   const long long pool_tokens = (long long)(a.contiguous ? p.B : p.num_pages) * p.page_size;
-  if (!(a.grouped ? grouped_kv_maps(&tm.kv, L.k_cache, L.v_cache, D, p.Hkv, pool_tokens, box, kBf16)
-                  : kv_maps(&tm.kv, L.k_cache, L.v_cache, D, p.Hkv, pool_tokens, box, kBf16)) ||
+  const auto encode_kv = a.grouped ? encode_grouped_kv_map : encode_kv_map;
+  if (!encode_kv(&tm.kv.k, L.k_cache, D, p.Hkv, pool_tokens, box, kBf16) ||
+      !encode_kv(&tm.kv.v, L.v_cache, D, p.Hkv, pool_tokens, box, kBf16) ||
       !encode_q_map(&tm.q, L.q, D, p.Hq, L.total_q, a.G, a.TQ, kBf16))
     return MXA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -1145,6 +1122,7 @@ mxa_status_t launch_prefill(const PrefillLaunch &L, cudaStream_t stream) {
   a.window = L.window < p.max_seqlen_k ? L.window : p.max_seqlen_k;  // a longer one hides nothing
   a.sinks = L.window > 0 ? L.sinks : 0;
   a.unit_cost = L.plan.unit_cost;
+  a.max_positions = (int)prefill_positions(p, L.total_q);
   a.scale_log2 = L.scale * 1.4426950408889634f;
   const bool bf16 = p.dtype == MXA_BF16;
   if (p.D == 128) return bf16 ? launch_typed<128, true>(L, a, stream) : launch_typed<128, false>(L, a, stream);

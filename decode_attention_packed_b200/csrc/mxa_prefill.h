@@ -38,6 +38,7 @@ struct PrefillArgs {
   int max_seqlen_k;
   int causal, window, sinks;
   int unit_cost;               // fixed cost of a unit, in KV blocks
+  int max_positions;           // what total_q tokens make at most (prefill_positions)
   float scale_log2;
 };
 

@@ -276,8 +276,8 @@ MXA_API mxa_status_t mxa_decode_fwd_append(const void *q, void *k_cache, void *v
                                            size_t workspace_bytes, void *out, float *lse, void *stream);
 
 /* mxa_plan for a call with a sliding window (mxa_decode_fwd_window): a row
- * streams at most the blocks of its window and its sinks, so a long row is
- * not cut into more pieces than those blocks fill.  window >= 1, sinks >= 0.
+ * streams at most the blocks of its window and its sinks, however long it is,
+ * and is cut into pieces of two of them at least.  window >= 1, sinks >= 0.
  * Arguments and errors otherwise as mxa_plan. */
 MXA_API mxa_status_t mxa_plan_window(const mxa_decode_params_t *params, int window, int sinks, int num_splits,
                                      int sm_count, mxa_plan_t *plan);
@@ -325,9 +325,14 @@ MXA_API mxa_status_t mxa_decode_fwd_window(const void *q, void *k_cache, void *v
  * A query that sees no key gets O = 0 and LSE = -inf.  Weights enter the
  * product with V rounded once to the input type; sums, maxima and
  * accumulators are float32.
- * Device-side breaches (lengths, offsets, page ids) are confined and reported
- * as for mxa_decode_fwd_varlen.  Errors: MXA_ERR_INVALID_ARG,
- * MXA_ERR_UNSUPPORTED, MXA_ERR_WORKSPACE, MXA_ERR_CUDA. */
+ * cu_seqlens_q may end before total_q: the tokens behind the last row are
+ * padding, whose out and lse are left as they were, so that one captured call
+ * serves batches of up to total_q tokens and B rows (rows without tokens cost
+ * next to nothing).  Other device-side breaches (lengths, offsets, page ids)
+ * are confined and reported as for mxa_decode_fwd_varlen.  Errors: MXA_ERR_INVALID_ARG,
+ * MXA_ERR_UNSUPPORTED (head dims, heads, rows and pages as above; work of
+ * more than 2^30 blocks, or 32-bit counts that could overflow),
+ * MXA_ERR_WORKSPACE, MXA_ERR_CUDA. */
 MXA_API mxa_status_t mxa_prefill_fwd(const void *q, const int32_t *cu_seqlens_q, int total_q, const void *k_cache,
                                      const void *v_cache, const int32_t *block_table,
                                      const int32_t *cache_seqlens, const mxa_decode_params_t *params, float scale,
@@ -346,7 +351,8 @@ MXA_API size_t mxa_prefill_workspace_size(const mxa_decode_params_t *params, int
  *                  besides those it holds are written behind them; nothing
  *                  else is written
  *   cache_seqlens: device [B]: L_b, read only
- *   cu_seqlens_q : device [B + 1]: 0 = cu[0] <= cu[1] <= ... <= cu[B] = total_q
+ *   cu_seqlens_q : device [B + 1]: 0 = cu[0] <= cu[1] <= ... <= cu[B] <= total_q;
+ *                  tokens behind cu[B] are padding and get slot -1
  *   free_pages   : device [num_free] page ids, taken from the front in row
  *                  order (row 0's pages first)
  *   slots        : device [total_q], written: the flat cache slot

@@ -161,13 +161,15 @@ def append_kv(k_cache, v_cache, k_new, v_new, block_table, cache_seqlens, *, pag
     return kb, vb
 
 
-def extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, *, page_size: int, num_pages: int):
+def extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, *, page_size: int, num_pages: int,
+                  total_q: Optional[int] = None):
     """Pages and slots of a step's new tokens, one request and one token at a time.
 
     Returns (block_table, slots, new_seqlens, pages_used): the table with the
     pages each request needs for its new tokens taken from the front of
     free_pages in request order, every new token's flat slot page * page_size
-    + offset, the lengths after the step and the number of pages taken.  A
+    + offset, the lengths after the step and the number of pages taken.
+    Tokens behind the last request, up to total_q, get slot -1.  A
     request whose pages do not fit its table, or which the free list cannot
     serve (nor could it a request before it that needed pages), takes none.
     """
@@ -175,7 +177,7 @@ def extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, *, page_
     L = np.asarray(cache_seqlens, dtype=np.int64)
     cu = np.asarray(cu_seqlens_q, dtype=np.int64)
     free = np.asarray(free_pages, dtype=np.int64)
-    slots = np.full(int(cu[-1]), -1, dtype=np.int64)
+    slots = np.full(int(cu[-1]) if total_q is None else total_q, -1, dtype=np.int64)
     new = L.copy()
     used, ran_out = 0, False
     for b in range(L.size):

@@ -80,6 +80,18 @@ def test_tables_when_a_row_is_too_narrow():
     check(*problem([10, 40, 64, 0], [10, 40, 1, 9], 16, width=4), 16)
 
 
+def test_tables_give_padding_no_slot():
+    table, ctx, cu, free, pages = problem([20, 3, 0], [20, 3, 9], 16)
+    for total in (32, 33, 5000):
+        t = ints(table)
+        slots, lens, used = mxa.extend_tables(t, ints(ctx), ints(cu), ints(free), page_size=16, num_pages=pages, total_q=total)
+        torch.cuda.synchronize()
+        assert mxa.mxa_device_error(True) == mxa.MXA_OK
+        bt, sl, nl, us = oracle.extend_tables(table, ctx, cu, free, page_size=16, num_pages=pages, total_q=total)
+        assert np.array_equal(t.cpu().numpy(), bt) and np.array_equal(slots.cpu().numpy(), sl)
+        assert np.array_equal(lens.cpu().numpy(), nl) and used.tolist() == [us]
+
+
 def test_tables_report_a_bad_page():
     table, ctx, cu, free, pages = problem([20, 3], [20, 3], 16)
     free = free.copy()

@@ -94,3 +94,57 @@ def test_cache_write_wants_16_byte_tokens_and_takes_none():
     assert mxa._lib.mxa_cache_write(*call) == MXA_ERR_UNSUPPORTED
     call = [None, None, 1024, 1024, None, 0, 8, 128, 64, 16, mxa.MXA_BF16, None, None, None]
     assert mxa._lib.mxa_cache_write(*call) == MXA_OK  # no token: nothing to do
+
+
+PREFILL = ["q", "cu", "total_q", "k", "v", "table", "lens", "params", "scale", "causal", "window", "sinks", "ws", "ws_bytes",
+           "out", "lse", "stream"]
+
+
+def prefill_status(p, **kw):
+    call = dict(q=FAKE, cu=FAKE, total_q=9, k=FAKE, v=FAKE, table=FAKE, lens=FAKE, params=ctypes.byref(p), scale=1.0,
+                causal=1, window=0, sinks=0, ws=FAKE, ws_bytes=1 << 40, out=FAKE, lse=None, stream=None)
+    call.update(kw)
+    return mxa._lib.mxa_prefill_fwd(*[call[n] for n in PREFILL])
+
+
+@pytest.mark.parametrize("shape,code", [
+    (dict(B=-1), MXA_ERR_INVALID_ARG), (dict(q_len=0), MXA_ERR_INVALID_ARG), (dict(Hq=0), MXA_ERR_INVALID_ARG),
+    (dict(Hq=30), MXA_ERR_INVALID_ARG), (dict(dtype=2), MXA_ERR_INVALID_ARG), (dict(page_size=0), MXA_ERR_INVALID_ARG),
+    (dict(num_pages=0), MXA_ERR_INVALID_ARG), (dict(max_seqlen_k=-1), MXA_ERR_INVALID_ARG), (dict(B=0), MXA_ERR_INVALID_ARG),
+    (dict(D=96), MXA_ERR_UNSUPPORTED), (dict(Hq=129, Hkv=1), MXA_ERR_UNSUPPORTED), (dict(B=12289), MXA_ERR_UNSUPPORTED),
+    (dict(num_pages=2**28), MXA_ERR_UNSUPPORTED), (dict(max_seqlen_k=2**30), MXA_ERR_UNSUPPORTED),
+])
+def test_prefill_shape_refusals(shape, code):
+    p = params(**shape)
+    assert prefill_status(p) == code
+    assert mxa.mxa_prefill_workspace_size(p, 9) == mxa.SIZE_MAX
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(total_q=-1), MXA_ERR_INVALID_ARG), (dict(total_q=2**27), MXA_ERR_UNSUPPORTED),
+    (dict(causal=2), MXA_ERR_INVALID_ARG), (dict(window=-1), MXA_ERR_INVALID_ARG), (dict(sinks=-1), MXA_ERR_INVALID_ARG),
+    (dict(causal=0, window=5), MXA_ERR_INVALID_ARG), (dict(sinks=4), MXA_ERR_INVALID_ARG),
+    (dict(scale=float("nan")), MXA_ERR_INVALID_ARG), (dict(scale=float("inf")), MXA_ERR_INVALID_ARG),
+    (dict(table=None), MXA_ERR_INVALID_ARG),  # a contiguous cache has a row per request
+    (dict(q=None), MXA_ERR_INVALID_ARG), (dict(cu=None), MXA_ERR_INVALID_ARG), (dict(k=None), MXA_ERR_INVALID_ARG),
+    (dict(v=None), MXA_ERR_INVALID_ARG), (dict(lens=None), MXA_ERR_INVALID_ARG), (dict(out=None), MXA_ERR_INVALID_ARG),
+    (dict(q=ODD), MXA_ERR_INVALID_ARG), (dict(k=ODD), MXA_ERR_INVALID_ARG), (dict(v=ODD), MXA_ERR_INVALID_ARG),
+    (dict(out=ODD), MXA_ERR_INVALID_ARG), (dict(cu=ODD), MXA_ERR_INVALID_ARG), (dict(lens=ODD), MXA_ERR_INVALID_ARG),
+    (dict(table=ODD), MXA_ERR_INVALID_ARG), (dict(lse=ODD), MXA_ERR_INVALID_ARG),
+])
+def test_prefill_call_refusals(kw, code):
+    assert prefill_status(params(), **kw) == code
+
+
+def test_prefill_layout_refusals():
+    assert prefill_status(params(page_size=12, max_seqlen_k=12000)) == MXA_ERR_UNSUPPORTED
+    assert prefill_status(params(max_pages_per_seq=1023)) == MXA_ERR_INVALID_ARG
+    assert prefill_status(params(num_pages=4, page_size=16383), table=None) == MXA_ERR_INVALID_ARG
+    # 2^17 tokens over 2^20 keys on 64 KV heads: more work than is laid out
+    big = params(B=1, q_len=2**17, Hq=64 * 128, Hkv=64, page_size=1024, max_seqlen_k=2**20)
+    assert prefill_status(big, total_q=2**17) == MXA_ERR_UNSUPPORTED
+
+
+def test_prefill_without_tokens_is_nothing_to_do():
+    assert prefill_status(params(), total_q=0, q=None, cu=None, k=None, v=None, lens=None, out=None, ws=None) == MXA_OK
+    assert prefill_status(params(B=0), total_q=0) == MXA_OK
