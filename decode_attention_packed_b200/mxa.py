@@ -382,6 +382,7 @@ def decode(q, k_cache, v_cache, block_table, cache_seqlens, *, scale=None, causa
     if prepared is None:
         prepared = prepare(q, k_cache, block_table, max_seqlen_k=max_seqlen_k, num_splits=num_splits,
                            window=window, sinks=sinks)
+        _lend(prepared.workspace, stream)
     f32 = out_dtype == torch.float32 or (out is not None and out.dtype == torch.float32)
     if out is None:
         out = torch.empty(q.shape, dtype=torch.float32, device=q.device) if f32 else torch.empty_like(q)
@@ -461,7 +462,8 @@ def prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, ma
     tokens over the cache, which holds their keys and values already:
     q [total_q, Hq, D], row b's tokens at cu_seqlens_q[b] .. cu_seqlens_q[b + 1]
     - 1, its last ones among cache_seqlens[b] keys; max_seqlen_q >= every
-    row's count.  Rows of one token and of thousands may be mixed.
+    row's count.  Rows of one token and of thousands may be mixed, and
+    tokens behind the last row are padding that is not written.
 
     causal: a token sees the keys up to its own position.  window > 0 (causal
     only) leaves it its last `window` keys and the first `sinks` keys."""
@@ -470,16 +472,19 @@ def prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, ma
     if prepared is None:
         prepared = prepare_prefill(q, cu_seqlens_q, k_cache, block_table, max_seqlen_q=max_seqlen_q,
                                    max_seqlen_k=max_seqlen_k)
-        if stream is not None and not isinstance(stream, int):
-            prepared.workspace.record_stream(stream)
-    dev, dtype, B = torch.cuda.current_device(), q.dtype, prepared.params.B
-    _want(dev, q, "q", dtype)
-    _want(dev, k_cache, "k_cache", dtype)
+        _lend(prepared.workspace, stream)
+    p, dev, dtype = prepared.params, torch.cuda.current_device(), q.dtype
+    B = p.B
+    if dtype is not (torch.bfloat16 if p.dtype == MXA_BF16 else torch.float16):
+        raise TypeError("q must have the type that the call was prepared for")
+    _want(dev, prepared.workspace, "the prepared workspace", torch.uint8)
+    _want(dev, q, "q", dtype, (q.shape[0], p.Hq, p.D))
+    _want(dev, k_cache, "k_cache", dtype, (p.num_pages, p.page_size, p.Hkv, p.D))
     _want(dev, v_cache, "v_cache", dtype, k_cache.shape)
     _want(dev, cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
     _want(dev, cache_seqlens, "cache_seqlens", torch.int32, (B,))
     if block_table is not None:
-        _want(dev, block_table, "block_table", torch.int32, (B, prepared.params.max_pages_per_seq))
+        _want(dev, block_table, "block_table", torch.int32, (B, p.max_pages_per_seq))
     if out is None:
         out = torch.empty_like(q)
     else:
@@ -488,9 +493,16 @@ def prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, ma
         lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
     elif lse is not None:
         _want(dev, lse, "lse", torch.float32, (q.shape[1], q.shape[0]))
-    mxa_prefill_fwd(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, prepared.params, scale, causal,
+    mxa_prefill_fwd(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, p, scale, causal,
                     window, sinks, prepared.workspace, out, lse, stream)
     return out, lse
+
+
+def _lend(workspace: Optional[torch.Tensor], stream) -> None:
+    """Keep a call's own workspace from being handed out again while `stream`
+    (None: the current one, whose order keeps it) still uses it."""
+    if workspace is not None and stream is not None:
+        workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
 def _want(device: int, t: torch.Tensor, name: str, dtype, shape=None) -> None:
@@ -514,9 +526,10 @@ def extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, *, page_
     taken from the front of free_pages, in row order, and written into
     block_table [B, width] (all int32, on the device).
 
-    Returns (slots [total_q], new_seqlens [B], pages_used [1]), int32.  A row
-    whose pages do not fit its table or the free list takes none: its slots
-    are -1 and its length is unchanged."""
+    Returns (slots [total_q], new_seqlens [B], pages_used [1]), int32.  Tokens
+    behind the last row are padding with slot -1.  A row whose pages do not fit
+    its table or the free list takes none: its slots are -1 and its length is
+    unchanged."""
     dev, int32 = torch.cuda.current_device(), torch.int32
     _want(dev, block_table, "block_table", int32)
     B = block_table.shape[0]

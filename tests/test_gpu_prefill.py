@@ -262,3 +262,78 @@ def test_many_rows_most_of_them_idle(D):
             lengths[b] = q_lens[b] + b % 50
     inp, q, cu = draw(q_lens, lengths, Hq=2, Hkv=1, D=D, seed=1650)
     check(inp, q, cu, *run(inp, q, cu))
+
+
+def test_padding_behind_the_last_row_stays_as_it_was():
+    # one captured call with room for 8 rows and 96 tokens, replayed for smaller batches
+    inp, q, cu = draw([30, 0, 1, 40, 1, 0, 2, 22], [300, 9, 77, 40, 1000, 5, 2, 500], seed=1750)
+    total = 96
+    args = [x.cuda() for x in (q, cu, inp.k_cache, inp.v_cache, inp.block_table, inp.cache_seqlens)]
+    prep = mxa.prepare_prefill(args[0], args[1], args[2], args[4], max_seqlen_q=40, max_seqlen_k=inp.max_seqlen_k)
+    out, lse = torch.empty_like(args[0]), torch.empty((8, total), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mxa.prefill(*args, max_seqlen_q=40, prepared=prep, out=out, lse=lse)
+    for rows in (8, 5, 4, 1, 0):
+        end = int(cu[rows])
+        part = cu.clamp_max(end)
+        args[1].copy_(part)
+        out.fill_(7.0), lse.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert mxa.mxa_device_error(True) == mxa.MXA_OK
+        assert (out[end:] == 7).all() and (lse[:, end:] == 7).all()
+        if end:
+            check(inp, q[:end], part, out[:end].cpu(), lse[:, :end].cpu())
+
+
+def test_overlapping_rows_are_reported():
+    # offsets that fall back make thousands of rows out of the same tokens:
+    # more work than the call was laid out for, none of which is run
+    B, T, Hq, Hkv, D, page, width = 12000, 4096, 64, 8, 64, 1024, 128
+    k, v = (torch.zeros(4, page, Hkv, D, dtype=torch.float16, device="cuda") for _ in range(2))
+    q = torch.zeros(T, Hq, D, dtype=torch.float16, device="cuda")
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[1::2] = T
+    table = torch.zeros(B, width, dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), page * width, dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 7.0)
+    mxa.prefill(q, cu, k, v, table, lens, max_seqlen_q=T, causal=False, out=out)
+    torch.cuda.synchronize()
+    assert mxa.mxa_device_error(True) == mxa.MXA_ERR_INVALID_ARG
+    assert (out == 7).all()
+
+
+def test_a_prepared_call_refuses_other_shapes():
+    inp, q, cu = draw([4, 2], [40, 9])
+    qd, cd, k, v, table, lens = [x.cuda() for x in (q, cu, inp.k_cache, inp.v_cache, inp.block_table, inp.cache_seqlens)]
+    prep = mxa.prepare_prefill(qd, cd, k, table, max_seqlen_q=4)
+    mxa.prefill(qd, cd, k, v, table, lens, max_seqlen_q=4, prepared=prep)
+    for args in ((qd[:, :4].contiguous(), cd, k, v, table, lens), (qd, cd, k[:-1], v[:-1], table, lens),
+                 (qd, cd, k, v, table[:, :-1].contiguous(), lens)):
+        with pytest.raises(ValueError):
+            mxa.prefill(*args, max_seqlen_q=4, prepared=prep)
+    with pytest.raises(TypeError):
+        mxa.prefill(qd.half(), cd, k.half(), v.half(), table, lens, max_seqlen_q=4, prepared=prep)
+    with pytest.raises(ValueError):
+        host = mxa.Prepared(prep.params, None, prep.workspace.cpu())
+        mxa.prefill(qd, cd, k, v, table, lens, max_seqlen_q=4, prepared=host)
+    with pytest.raises(mxa.MxaError):  # more tokens than it was prepared for
+        small = mxa.Prepared(prep.params, None, prep.workspace[:256])
+        mxa.prefill(qd, cd, k, v, table, lens, max_seqlen_q=4, prepared=small)
+
+
+def test_a_stream_given_by_hand():
+    inp, q, cu = draw([200, 1, 60], [2000, 3000, 60], seed=1900)
+    first = run(inp, q, cu)
+    args = [x.cuda() for x in (q, cu, inp.k_cache, inp.v_cache, inp.block_table, inp.cache_seqlens)]
+    out, lse = torch.empty_like(args[0]), torch.empty((8, 261), device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        out.zero_()
+        torch.cuda.synchronize()
+        mxa.prefill(*args, max_seqlen_q=200, max_seqlen_k=inp.max_seqlen_k, out=out, lse=lse, stream=stream)
+        torch.empty(64 << 20, dtype=torch.uint8, device="cuda").fill_(255)  # what the current stream allocates meanwhile
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu().view(torch.int16), first[0].view(torch.int16)) and torch.equal(lse.cpu(), first[1])
