@@ -69,18 +69,19 @@ struct Cfg {
   static_assert(kSlots % 2 == 0, "keys in the even slots, values in the odd ones");
   static constexpr int kQBytes = kTileRows * D * 2;
   // Tensor memory: NS score buffers of T columns, two weight buffers of T / 2
-  // (a column holds two weights of a row), then the tiles' accumulators.  At
-  // D = 128 the two tiles' scores take turns in one buffer: it is free again
-  // as soon as they are in registers.
-  static constexpr int NS = D == 128 ? 1 : 2;
+  // (a column holds two weights of a row), then the tiles' accumulators.  Two
+  // tiles' scores take turns in one buffer, which is free again as soon as
+  // they are in registers.  The turns keep the tiles out of step, so that one's
+  // exponentials run beside the other's loads and stores: with a buffer each
+  // (room for it at D = 64) a block took 3550 cycles instead of 3250.
+  static constexpr int NS = D <= 128 ? 1 : 2;
   static constexpr int kPCol = NS * T, kOCol = 512 - NT * D;
   static_assert(kPCol + T <= kOCol, "tensor memory");
   // shared memory
   static constexpr int kQOff = kSlots * kSlotBytes;
-  // 2 KB a softmax warp: maxima and sums for the other half of its rows, and
-  // the rows it writes out
+  // two places a softmax warp for maxima and sums, for the other half of its rows
   static constexpr int kStageOff = kQOff + NT * kQBytes;
-  static constexpr int kDescOff = kStageOff + kSoftmaxWarps * 2048;
+  static constexpr int kDescOff = kStageOff + kSoftmaxWarps * 256;
   static constexpr int kBarOff = kDescOff + kDescs * 64;
   static constexpr int kSmem = kBarOff + 512;
   // barriers
@@ -98,8 +99,8 @@ struct Segment {
   int q0, qn, L;     // the row's first packed token, its tokens and its keys
   int beg, end;      // blocks [beg, end) of the unit's own numbering
   int kind;          // 0: the whole unit; 1 / 2: piece in the CTA's head / tail slot; -1: no more work
-  int c_first, n_pieces;
-  int pad[5];
+  int x, nb, per_cta;  // position of the unit's first block, its blocks, and the ranges' length
+  int pad[4];
 };
 static_assert(sizeof(Segment) == 64, "descriptor slot");
 
@@ -179,9 +180,9 @@ __device__ Segment walk_take(const PrefillArgs &a, Walk &w, int lane) {
   s.beg = w.blk;
   s.end = w.blk + len;
   s.kind = (s.beg == 0 && s.end == w.nb) ? 0 : s.beg > 0 ? 1 : 2;
-  const int xs = w.x - w.blk;
-  s.c_first = xs / w.per_cta;
-  s.n_pieces = (xs + w.nb - 1) / w.per_cta - s.c_first + 1;
+  s.x = w.x - w.blk;
+  s.nb = w.nb;
+  s.per_cta = w.per_cta;
   w.x += len;
   w.blk += len;
   if (w.blk == w.nb && w.x < w.end) {
@@ -237,46 +238,52 @@ __device__ __forceinline__ int row_positions(const PrefillArgs &a, int b, int la
 // This CTA's range, from the rows' positions (`rows`, of one KV head each, in
 // shared memory); one warp.
 template <int D>
-__device__ Walk walk_start(const PrefillArgs &a, int *rows, int lane) {
+__device__ Walk walk_start(const PrefillArgs &a, const int *rows, int lane) {
   constexpr int NT = Cfg<D>::NT;
   Walk w;
   w.b = w.h = w.it = w.tiles = w.q0 = w.qn = w.L = w.blk = w.nb = 0;
   w.x = w.end = 0;
   w.per_cta = 1;
-  const int chunk = (a.B + 31) / 32;
-  const int lo = min(lane * chunk, a.B), hi = min(lo + chunk, a.B);
-  long long sum = 0;
-  for (int i = lo; i < hi; ++i) sum += rows[i];
-  long long incl = sum;
+  // Sums stop at the bound that total_q tokens cannot pass, so that they stay
+  // in 32 bits whatever the offsets say.
+  auto scan = [&](int v) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  const long long all = __shfl_sync(0xffffffffu, incl, 31) * a.Hkv;
-  // More than total_q tokens can make: rows overlap (check_row has reported
-  // their offsets), and nothing is run.  Below the bound 32 bits are enough.
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = min(v + u, a.max_positions + 1);
+    }
+    return v;
+  };
+  // each lane's share of the rows, then the lane and the row that hold x0
+  const int chunk = (a.B + 31) / 32;
+  const int lo = lane * chunk, hi = min(lo + chunk, a.B);
+  int sum = 0;
+  for (int i = lo; i < hi; ++i) sum = min(sum + rows[i], a.max_positions + 1);
+  const int incl = scan(sum);
+  const int all = __shfl_sync(0xffffffffu, incl, 31);
+  // past the bound: rows overlap (check_row reports their offsets); nothing is run
   if (all == 0 || all > a.max_positions) return w;
-  const int total = (int)all;
-  int run = (int)(incl - sum);
-  for (int i = lo; i < hi; ++i) {
-    run += rows[i];
-    rows[i] = run;
-  }
-  __syncwarp();
+  const int total = all * a.Hkv;
   w.per_cta = (total + (int)gridDim.x - 1) / (int)gridDim.x;
   const int x0 = blockIdx.x * w.per_cta;
   if (x0 >= total) return w;
   w.end = min(w.per_cta, total - x0) + x0;
-  int b0 = 0, b1 = a.B - 1;  // first row whose positions end past x0
-  while (b0 < b1) {
-    const int mid = (b0 + b1) >> 1;
-    if (rows[mid] * a.Hkv > x0) b1 = mid; else b0 = mid + 1;
+  const int owner = __ffs(__ballot_sync(0xffffffffu, incl * a.Hkv > x0)) - 1;
+  int pre = __shfl_sync(0xffffffffu, incl - sum, owner), width = 0;  // positions before the row, and its own
+  for (int i = owner * chunk;; i += 32) {
+    const int n = i + lane < min((owner + 1) * chunk, a.B) ? rows[i + lane] : 0, upto = pre + scan(n);
+    const unsigned past = __ballot_sync(0xffffffffu, upto * a.Hkv > x0);
+    if (past != 0) {
+      const int l = __ffs(past) - 1;
+      w.b = i + l;
+      width = __shfl_sync(0xffffffffu, n, l);
+      pre = __shfl_sync(0xffffffffu, upto, l) - width;
+      break;
+    }
+    pre = __shfl_sync(0xffffffffu, upto, 31);
   }
-  w.b = b0;
   row_of(a, w.b, w.q0, w.qn, w.L);
   w.tiles = (w.qn + NT * a.TQ - 1) / (NT * a.TQ);
-  const int pre = w.b > 0 ? rows[w.b - 1] : 0, width = rows[w.b] - pre;
   const int off = x0 - pre * a.Hkv;
   w.h = off / width;
   const int in_head = off - w.h * width;
@@ -612,6 +619,18 @@ __device__ bool issue_values(const PrefillArgs &a, uint8_t *smem, uint32_t tmem,
   }
 }
 
+// 32 bytes to global memory: one store where the address allows it.
+__device__ __forceinline__ void store_sector(void *p, const uint32_t *w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(__cvta_generic_to_global(p)), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 // n ones from bit 0 up, for any n.
 __device__ __forceinline__ uint32_t bits_below(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
@@ -631,8 +650,8 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
   const int r_tok = r / a.G, r_head = r - r_tok * a.G;   // its token and head
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;    // this warp's lanes of tensor memory
   const uint32_t o_addr = tmem + lanes + C::kOCol + t * D + half * DH;
-  uint8_t *stage = smem + C::kStageOff + ((t * 2 + half) * 4 + warp) * 2048;
-  const uint8_t *other = smem + C::kStageOff + ((t * 2 + (half ^ 1)) * 4 + warp) * 2048;
+  uint8_t *stage = smem + C::kStageOff + ((t * 2 + half) * 4 + warp) * 256;
+  const uint8_t *other = smem + C::kStageOff + ((t * 2 + (half ^ 1)) * 4 + warp) * 256;
   const int xchg = C::B_XCHG + t * 4 + warp;
   int x_n = 0;  // exchanges with the warp that has the rows' other halves
   // The issuing warp has negated the scores for a negative scale.  A zero scale
@@ -715,21 +734,23 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
             for (int i = 0; i < 32; ++i) x[c + i] = (seen >> i) & 1u ? x[c + i] : -INFINITY;
           }
         }
-        const int b0 = s.it * NT * a.TQ;
-        const Steps st = steps_of<T>(a, span_of<T>(a, s.L, s.qn, b0, min(b0 + NT * a.TQ, (int)s.qn)), j0);
-        if (t == 0 && st.clear) {  // values of hidden keys become zeros
-          const int sl = slot_n % C::kSlots;
-          if (!wait(C::B_FULL + sl, slot_n / C::kSlots)) return false;
-          const uint32_t v = sbase + sl * C::kSlotBytes;
+        if (t == 0) {
+          const int b0 = s.it * NT * a.TQ;
+          const Steps st = steps_of<T>(a, span_of<T>(a, s.L, s.qn, b0, min(b0 + NT * a.TQ, (int)s.qn)), j0);
+          if (st.clear) {  // values of hidden keys, [g0, g1) and [top, ..) of the steps, become zeros
+            const int sl = slot_n % C::kSlots;
+            if (!wait(C::B_FULL + sl, slot_n / C::kSlots)) return false;
+            const uint32_t v = sbase + sl * C::kSlotBytes;
+            const int from = max(st.g0, st.k0 * 16), gap = max(0, st.g1 - from), keys = gap + st.k1 * 16 - st.top;
 #pragma unroll 1
-          for (int i = st.k0 * 16 * (D / 8) + half * kTileRows + r; i < st.k1 * 16 * (D / 8); i += 2 * kTileRows) {
-            const int key = i / (D / 8), c = i % (D / 8);
-            if (key >= st.top || (key >= st.g0 && key < st.g1))
+            for (int i = half * kTileRows + r; i < keys * (D / 8); i += 2 * kTileRows) {
+              const int n = i / (D / 8), c = i % (D / 8), key = n < gap ? from + n : st.top + n - gap;
               asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + (key / 8) * C::kGroupBytes + (c / 8) * 1024 + (key % 8) * 128 + (c % 8) * 16),
                            "r"(0u) : "memory");
+            }
+            fence_proxy_async_smem();  // before the product reads them
+            __syncwarp();
           }
-          fence_proxy_async_smem();  // before the product reads them
-          __syncwarp();
         }
       }
       slot_n += 2;
@@ -796,15 +817,12 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     float l_other;
     if (!exchange(l, l_other)) return false;
     l = half == 0 ? l + l_other : l_other + l;  // the same sum in both halves
-    // and once more, before the rows overwrite the place of the sums
-    if (!exchange(0.f, l_other)) return false;
     const float inv = l == 0.f ? 0.f : rcp(l);
     const int hq = s.h * a.G + r_head, v0 = s.it * NT * a.TQ, tok = v0 + t * a.TQ + r_tok;
     const bool real = r_tok < a.TQ && tok < s.qn;
     // Where the row goes: row `row` of the output, or of the CTA's piece slot.
     const int row0 = s.kind == 0 ? (s.q0 + tok) * a.Hq + hq
                                  : (blockIdx.x * 2 + (s.kind - 1)) * (NT * kTileRows) + t * kTileRows + r;
-    const int row = real ? row0 : -1;
     if (real && half == 0) {
       const float lse = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
       if (s.kind != 0) a.lse_part[row0] = lse;
@@ -817,50 +835,35 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
       pd.h = s.h;
       pd.t0 = v0;
       pd.tokens = min(NT * a.TQ, s.qn - v0);
-      pd.c_first = s.c_first;
-      pd.n_pieces = s.n_pieces;
+      pd.c_first = s.x / s.per_cta;
+      pd.n_pieces = (s.x + s.nb - 1) / s.per_cta - pd.c_first + 1;
     }
     const int lu = NT == 2 ? t : (blk_n - 1) & 1;  // the last block's values
     if (!wait(C::B_OFULL + lu, NT == 2 ? blk_n - 1 : (blk_n - 1) >> 1)) return false;
     tc_fence_after();
-    // 16 columns of every row at a time, through shared memory (16-byte chunks
-    // swizzled by the row), so that 2 or 4 lanes write a row's bytes
-    // together: a lane writing its own row would touch 32 lines with every
-    // store.  A short loop: code that runs once a unit is fetched anew.
+    // A lane writes its row's half, 32 bytes in a store: whole sectors, without
+    // a detour through shared memory.  A short loop: code that runs once a unit
+    // is fetched anew.
     const bool piece = s.kind != 0;
-    const int shift = piece ? 2 : 1;  // log2 of a row's 16-byte chunks a step, and of a value's bytes
-    uint8_t *dst = (piece ? reinterpret_cast<uint8_t *>(a.o_part) : static_cast<uint8_t *>(a.out)) + ((half * DH) << shift);
-    const int c = lane & ((1 << shift) - 1);
+    uint8_t *dst = piece ? reinterpret_cast<uint8_t *>(a.o_part + (size_t)row0 * D + half * DH)
+                         : static_cast<uint8_t *>(a.out) + ((size_t)row0 * D + half * DH) * 2;
 #pragma unroll 1
-    for (int col = 0; col < DH; col += 16) {
-      float o[16];
-      tmem_ld16(o_addr + col, reinterpret_cast<uint32_t *>(o));
+    for (int col = 0; col < DH; col += 32) {
+      float o[32];
+      tmem_ld32(o_addr + col, reinterpret_cast<uint32_t *>(o));
       tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;  // no key: O holds nothing to read
-      __syncwarp();
+      for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;  // no key: O holds nothing to read
+      if (!real) continue;
       if (piece) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<float4 *>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-              make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        for (int i = 0; i < 32; i += 8) store_sector(dst + (col + i) * 4, reinterpret_cast<const uint32_t *>(o + i), true);
       } else {
+        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<uint4 *>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-              make_uint4(pack2<kBf16>(o[8 * i], o[8 * i + 1]), pack2<kBf16>(o[8 * i + 2], o[8 * i + 3]),
-                         pack2<kBf16>(o[8 * i + 4], o[8 * i + 5]), pack2<kBf16>(o[8 * i + 6], o[8 * i + 7]));
-      }
-      __syncwarp();
+        for (int i = 0; i < 16; ++i) w[i] = pack2<kBf16>(o[2 * i], o[2 * i + 1]);
 #pragma unroll
-      for (int k = 0; k < 4; k += 2) {  // two rows in flight (16-bit rows are done after two)
-        if (k > 0 && !piece) break;
-        const int ra = (lane >> shift) + k * (32 >> shift), rb = ra + (32 >> shift);
-        const int ta = __shfl_sync(0xffffffffu, row, ra), tb = __shfl_sync(0xffffffffu, row, rb);
-        const uint4 va = *reinterpret_cast<const uint4 *>(stage + ra * 64 + ((c ^ ((ra >> 1) & 3)) << 4));
-        const uint4 vb = *reinterpret_cast<const uint4 *>(stage + rb * 64 + ((c ^ ((rb >> 1) & 3)) << 4));
-        if (ta >= 0) *reinterpret_cast<uint4 *>(dst + (((size_t)ta * D + col) << shift) + c * 16) = va;
-        if (tb >= 0) *reinterpret_cast<uint4 *>(dst + (((size_t)tb * D + col) << shift) + c * 16) = vb;
+        for (int i = 0; i < 16; i += 8) store_sector(dst + (col + 2 * i) * 2, w + i, a.wide_out);
       }
     }
     tc_fence_before();  // the accumulator has been read before this thread's next arrival
@@ -1121,8 +1124,9 @@ mxa_status_t launch_prefill(const PrefillLaunch &L, cudaStream_t stream) {
   a.causal = L.causal;
   a.window = L.window < p.max_seqlen_k ? L.window : p.max_seqlen_k;  // a longer one hides nothing
   a.sinks = L.window > 0 ? L.sinks : 0;
+  a.wide_out = reinterpret_cast<uintptr_t>(L.out) % 32 == 0;
   a.unit_cost = L.plan.unit_cost;
-  a.max_positions = (int)prefill_positions(p, L.total_q);
+  a.max_positions = (int)(prefill_positions(p, L.total_q) / p.Hkv);
   a.scale_log2 = L.scale * 1.4426950408889634f;
   const bool bf16 = p.dtype == MXA_BF16;
   if (p.D == 128) return bf16 ? launch_typed<128, true>(L, a, stream) : launch_typed<128, false>(L, a, stream);

@@ -37,8 +37,9 @@ struct PrefillArgs {
   int grouped;                 // boxes of whole keys (rows at multiples of 8 tokens), else of one chunk
   int max_seqlen_k;
   int causal, window, sinks;
+  int wide_out;                // out lies at a multiple of 32 bytes
   int unit_cost;               // fixed cost of a unit, in KV blocks
-  int max_positions;           // what total_q tokens make at most (prefill_positions)
+  int max_positions;           // what total_q tokens make at most on one KV head
   float scale_log2;
 };
 
