@@ -4,9 +4,9 @@
 //   O = softmax(scale Q K^T + mask) V,   LSE = ln sum_j exp(scale q . k_j)
 //
 // Each CTA walks a contiguous share of the work with these roles:
-//  - a producer warp finds the CTA's share, gathers K and V pages through the
-//    block table with TMA into a ring of shared-memory slots; a query warp
-//    loads the packed query rows;
+//  - two loading warps, one of which finds the CTA's share, gather K and V
+//    pages through the block table with TMA into a ring of shared-memory slots
+//    and load the packed query rows;
 //  - two issuing warps run S = Q K^T and O += P V on the tensor cores
 //    (tcgen05, accumulators and P in tensor memory);
 //  - softmax warps, two threads per packed query row, turn S into P with a
@@ -62,7 +62,7 @@ struct Cfg {
   static constexpr int kGroupBytes = CH * 1024;
   static constexpr int kSoftmaxWarps = 8 * NT;      // two threads a row
   static constexpr int kScoreWarp = kSoftmaxWarps, kValueWarp = kSoftmaxWarps + 1;
-  static constexpr int kProducerWarp = kSoftmaxWarps + 2;  // and the query warp
+  static constexpr int kKeyWarp = kSoftmaxWarps + 2;  // and the one that loads queries and values
   static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
   static constexpr int kSlotBytes = T * D * 2;      // one block of K or of V
   static constexpr int kSlots = 128 * 1024 / kSlotBytes;
@@ -93,7 +93,7 @@ struct Cfg {
   static_assert(B_COUNT * 8 + 16 <= 512 && kSmem <= 227 * 1024, "shared memory");
 };
 
-// A contiguous range of one unit's KV blocks, as the producer publishes it.
+// A contiguous range of one unit's KV blocks, as the key warp publishes it.
 struct Segment {
   int b, h, it;      // batch row, KV head, group of tiles
   int q0, qn, L;     // the row's first packed token, its tokens and its keys
@@ -334,131 +334,132 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
 }
 
 // ---------------------------------------------------------------------------
-// Producer warp
+// Loading warps: one finds the CTA's share, publishes its segments and loads
+// their keys; the other loads each segment's queries, once the unit before has
+// issued its last scores, and its values.  Two, because issuing is what bounds
+// them: a box takes a warp 50 to 120 cycles whatever its size, and at 16 tokens
+// a page a single warp set the pace of the whole kernel (3200 cycles a block
+// at D = 64).
 // ---------------------------------------------------------------------------
-template <int D, bool kBf16>
-__device__ bool producer(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *smem, int lane) {
+template <int D>
+__device__ bool loader(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *smem, bool values, int lane) {
   using C = Cfg<D>;
-  constexpr int T = C::T;
+  constexpr int T = C::T, NT = C::NT;
   const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
   Segment *descs = reinterpret_cast<Segment *>(smem + C::kDescOff);
-  Walk w = walk_start<D>(a, reinterpret_cast<int *>(smem), lane);
-  fence_proxy_async_smem();  // the scan's accesses precede the ring's loads
-  __syncwarp();
-  const int bt = a.box_tokens;
-  int slot_n = 0, seg_n = 0;
-  bool ok = true, bad_page = false;
-  // page of the box at token `tok` of row b, for this lane
-  auto page_at = [&](int b, int tok) {
-    const int p = tok / a.page_size;
-    return p < a.mpps ? a.block_table[(size_t)b * a.mpps + p] : -1;
-  };
-  for (;;) {
-    const bool more = w.x < w.end;
-    const Walk at = w;
-    Segment s;
-    if (more) s = walk_take<D>(a, w, lane);
-    else s.kind = -1;
-    const int d = seg_n % kDescs;
-    if (!wait_phase(bars + 8 * (C::B_DEMPTY + d), ((seg_n / kDescs) & 1) ^ 1)) {
-      ok = false;
-      break;
-    }
-    if (lane == 0) {
-      descs[d] = s;
-      mbar_arrive(bars + 8 * (C::B_DFULL + d));
-    }
+  Walk w;
+  if (!values) {
+    w = walk_start<D>(a, reinterpret_cast<int *>(smem), lane);
+    fence_proxy_async_smem();  // the scan's accesses precede the ring's loads
     __syncwarp();
-    if (!more) break;
-    ++seg_n;
-    const Span span = walk_span<D>(a, at);
-    int page = 0;
-    if (!a.contiguous && lane < T / bt) page = page_at(s.b, span.block(s.beg) * T + lane * bt);
-    for (int blk = s.beg; blk < s.end && ok; ++blk) {
-      const int tok0 = span.block(blk) * T;
+  }
+  const void *map = values ? (const void *)&tm.kv.v : (const void *)&tm.kv.k;
+  const int bt = a.box_tokens, ps = a.page_size;
+  const int pages = T / ps, rest = T % ps;  // a block's length in pages
+  const bool has_box = lane < T / bt;       // this lane has box `lane` of a block
+  int slot = values ? 1 : 0, phase = 1;     // ring slot of the next block, and the phase that frees it
+  int loaded = 0, seg_n = 0;
+  bool ok = true, bad_page = false;
+  auto page_of = [&](int b, int p) { return has_box && p < a.mpps ? a.block_table[(size_t)b * a.mpps + p] : -1; };
+  for (;; ++seg_n) {
+    const int d = seg_n % kDescs;
+    Segment s;
+    if (!values) {
+      if (w.x < w.end) s = walk_take<D>(a, w, lane);
+      else s.kind = -1;
+      if (!(ok = wait_phase(bars + 8 * (C::B_DEMPTY + d), ((seg_n / kDescs) & 1) ^ 1))) break;
+      if (lane == 0) {
+        descs[d] = s;
+        mbar_arrive(bars + 8 * (C::B_DFULL + d));
+      }
+      __syncwarp();
+    } else {
+      if (!(ok = wait_phase(bars + 8 * (C::B_DFULL + d), (seg_n / kDescs) & 1))) break;
+      s = descs[d];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (C::B_DEMPTY + d));
+    }
+    if (s.kind < 0) break;
+    const int t0 = s.it * NT * a.TQ;
+    const Span span = span_of<T>(a, s.L, s.qn, t0, min(t0 + NT * a.TQ, s.qn));
+    // place of this lane's box: entry p of the row's table, token `off` of the page
+    int p = 0, off = 0, page = 0;
+    auto seek = [&](int blk) {
+      const int tok = span.block(blk) * T + lane * bt;
+      p = tok / ps;
+      off = tok - p * ps;
+    };
+    if (!a.contiguous) {
+      seek(s.beg);
+      page = page_of(s.b, p);
+    }
+    if (values) {
+      if (!(ok = wait_phase(bars + 8 * C::B_QEMPTY, (seg_n & 1) ^ 1))) break;
+      const int tiles = min(NT, (s.qn - t0 + a.TQ - 1) / a.TQ);
+      if (lane == 0) mbar_arrive_expect_tx(bars + 8 * C::B_QFULL, (uint32_t)(tiles * C::CH * a.TQ * a.G * 128));
+      __syncwarp();
+      if (lane < tiles * C::CH) {
+        const int t = lane / C::CH, ch = lane % C::CH;
+        tma_load_3d(sbase + C::kQOff + t * C::kQBytes + ch * (kTileRows * 128), &tm.q, ch * 64, s.h * a.G,
+                    s.q0 + t0 + t * a.TQ, bars + 8 * C::B_QFULL);
+      }
+    }
+    for (int blk = s.beg; blk < s.end; ++blk) {
+      const int tok0 = span.block(blk) * T, tok = tok0 + lane * bt;
       const int valid = max(0, min(T, span.hi - tok0));
       const int nbox = (valid + bt - 1) / bt;
-      int next_page = 0;  // of the next block, on its way while this one is issued
-      if (!a.contiguous && blk + 1 < s.end && lane < T / bt) next_page = page_at(s.b, span.block(blk + 1) * T + lane * bt);
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const int sl = slot_n % C::kSlots;
-        const uint32_t full = bars + 8 * (C::B_FULL + sl);
-        if (!wait_phase(bars + 8 * (C::B_EMPTY + sl), ((slot_n / C::kSlots) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(nbox * bt * D * 2));
-        __syncwarp();
-        const void *map = kv ? (const void *)&tm.kv.v : (const void *)&tm.kv.k;
-        const int box = a.grouped ? lane : lane / C::CH, ch = a.grouped ? 0 : lane % C::CH;
-        for (int b0 = 0; b0 < nbox; b0 += a.grouped ? 32 : 32 / C::CH) {
-          const int tok = tok0 + (b0 + box) * bt;
-          int pg = __shfl_sync(0xffffffffu, page, (b0 + box) & 31);
-          int row = s.b * a.page_size + tok;
-          if (!a.contiguous) {
-            // A box of hidden keys only is never read, whatever its table entry
-            // holds; a page outside the pool reads as zeros and is reported.
-            // Both are placed at negative rows, which the map fills with zeros.
-            const bool hidden = tok >= a.sinks && tok + bt <= span.low;
-            if (hidden || pg < 0 || pg >= a.num_pages) {
-              bad_page |= !hidden && b0 + box < nbox;
-              pg = -1;
+      int row = s.b * ps + tok;
+      if (!a.contiguous) {
+        // A box of hidden keys only is never read, whatever its table entry
+        // holds; a page outside the pool reads as zeros and is reported.
+        // Both are placed at negative rows, which the map fills with zeros.
+        const bool hidden = tok >= a.sinks && tok + bt <= span.low;
+        const bool there = !hidden && page >= 0 && page < a.num_pages;
+        bad_page |= !hidden && !there && lane < nbox;
+        row = (there ? page * ps : -ps) + off;
+        // the next block's page is on its way while this block is issued; the
+        // places step on without a division
+        if (blk + 1 < s.end) {
+          if (blk + 1 == span.ns) {
+            seek(blk + 1);
+          } else {
+            p += pages;
+            off += rest;
+            if (off >= ps) {
+              off -= ps;
+              ++p;
             }
-            row = pg < 0 ? -a.page_size + tok % a.page_size : pg * a.page_size + tok % a.page_size;
           }
-          const uint32_t dst = sbase + sl * C::kSlotBytes + (b0 + box) * (bt / 8) * C::kGroupBytes + ch * 1024;
-          if (b0 + box < nbox) {
-            if (a.grouped) tma_load_4d(dst, map, 0, 0, s.h * C::CH, row >> 3, full);
-            else tma_load_3d(dst, map, ch * 64, s.h, row, full);
-          }
+          page = page_of(s.b, p);
         }
-        ++slot_n;
       }
-      page = next_page;
+      const uint32_t full = bars + 8 * (C::B_FULL + slot);
+      if (!(ok = wait_phase(bars + 8 * (C::B_EMPTY + slot), phase))) break;
+      if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(nbox * bt * D * 2));
+      __syncwarp();
+      if (lane < nbox) {
+        const uint32_t dst = sbase + slot * C::kSlotBytes + lane * (bt / 8) * C::kGroupBytes;
+        if (a.grouped) {
+          tma_load_4d(dst, map, 0, 0, s.h * C::CH, row >> 3, full);
+        } else {
+#pragma unroll 1
+          for (int ch = 0; ch < C::CH; ++ch) tma_load_3d(dst + ch * 1024, map, ch * 64, s.h, row, full);
+        }
+      }
+      ++loaded;
+      slot += 2;
+      if (slot >= C::kSlots) {
+        slot -= C::kSlots;
+        phase ^= 1;
+      }
     }
     if (!ok) break;
   }
   if (__any_sync(0xffffffffu, bad_page) && lane == 0) atomicOr(a.err, kErrBadPage);
   // Leave only when the copies issued here have landed.
-  for (int j = max(0, slot_n - C::kSlots); j < slot_n; ++j)
-    ok &= wait_phase(bars + 8 * (C::B_FULL + j % C::kSlots), (j / C::kSlots) & 1);
-  return ok;
-}
-
-// ---------------------------------------------------------------------------
-// Query warp: a unit's packed rows, as soon as the unit before has issued its
-// last scores.  A warp of its own, so that the next unit's first keys and
-// values are on their way before that.
-// ---------------------------------------------------------------------------
-template <int D>
-__device__ bool queries(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *smem, int lane) {
-  using C = Cfg<D>;
-  constexpr int NT = C::NT;
-  const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
-  const Segment *descs = reinterpret_cast<const Segment *>(smem + C::kDescOff);
-  int seg_n = 0;
-  bool ok = true;
-  for (;; ++seg_n) {
-    const int d = seg_n % kDescs;
-    if (!(ok = wait_phase(bars + 8 * (C::B_DFULL + d), (seg_n / kDescs) & 1))) break;
-    const Segment s = descs[d];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bars + 8 * (C::B_DEMPTY + d));
-    if (s.kind < 0) break;
-    if (!(ok = wait_phase(bars + 8 * C::B_QEMPTY, (seg_n & 1) ^ 1))) break;
-    const int t0 = s.it * NT * a.TQ;
-    const int tiles = min(NT, (s.qn - t0 + a.TQ - 1) / a.TQ);
-    if (lane == 0) mbar_arrive_expect_tx(bars + 8 * C::B_QFULL, (uint32_t)(tiles * C::CH * a.TQ * a.G * 128));
-    __syncwarp();
-    if (lane < tiles * C::CH) {
-      const int t = lane / C::CH, ch = lane % C::CH;
-      tma_load_3d(sbase + C::kQOff + t * C::kQBytes + ch * (kTileRows * 128), &tm.q, ch * 64, s.h * a.G,
-                  s.q0 + t0 + t * a.TQ, bars + 8 * C::B_QFULL);
-    }
-  }
-  // leave only when the copies issued here have landed
-  if (seg_n > 0) ok &= wait_phase(bars + 8 * C::B_QFULL, (seg_n - 1) & 1);
+  for (int j = max(0, loaded - C::kSlots / 2); j < loaded; ++j)
+    ok &= wait_phase(bars + 8 * (C::B_FULL + 2 * (j % (C::kSlots / 2)) + (values ? 1 : 0)), (j / (C::kSlots / 2)) & 1);
+  if (values && seg_n > 0) ok &= wait_phase(bars + 8 * C::B_QFULL, (seg_n - 1) & 1);
   return ok;
 }
 
@@ -904,7 +905,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     fence_mbar_init();
   }
   if (warp == C::kScoreWarp) tmem_alloc(tmem_slot, 512);
-  if (tid == 32 * C::kProducerWarp) {
+  if (tid == 32 * C::kKeyWarp) {
     prefetch_tmap(&tm.kv.k);
     prefetch_tmap(&tm.kv.v);
     prefetch_tmap(&tm.q);
@@ -913,7 +914,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   // Inputs may be written, and outputs and workspace used, by the kernel
   // this launch depends on.
   grid_dependency_wait();
-  // the rows' positions, for the producer's scan (the ring is still unused)
+  // the rows' positions, for the key warp's scan (the ring is still unused)
   int *rows = reinterpret_cast<int *>(smem);
   for (int b = warp * 32; b < a.B; b += C::kThreads) {
     const int n = row_positions<D>(a, b, lane);
@@ -935,8 +936,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     if constexpr (C::NT == 2) regs_dec<64>();  // 96 a thread at launch: 640 x 96 = 512 x 104 + 128 x 64
     if (warp == C::kScoreWarp) ok = issue_scores<D, kBf16>(a, smem, tmem, lane);
     else if (warp == C::kValueWarp) ok = issue_values<D, kBf16>(a, smem, tmem, lane);
-    else if (warp == C::kProducerWarp) ok = producer<D, kBf16>(tm, a, smem, lane);
-    else ok = queries<D>(tm, a, smem, lane);
+    else ok = loader<D>(tm, a, smem, warp != C::kKeyWarp, lane);
   } else {
     if constexpr (C::NT == 2) regs_inc<104>();
     ok = softmax<D, kBf16>(a, smem, tmem, warp / 8, (warp / 4) % 2, warp % 4, lane);
