@@ -9,8 +9,8 @@
 //    and load the packed query rows;
 //  - two issuing warps run S = Q K^T and O += P V on the tensor cores
 //    (tcgen05, accumulators and P in tensor memory);
-//  - softmax warps, two threads per packed query row, turn S into P with a
-//    running maximum and sum, and write the rows out.
+//  - softmax warps, one thread per packed query row (two for head dim 256),
+//    turn S into P with a running maximum and sum, and write the rows out.
 //
 // Units.  The G query heads of one KV head are packed into the rows of a
 // tile, row m = t * G + g, so a KV byte serves all of them: a 128-row tile
@@ -60,7 +60,11 @@ struct Cfg {
   // chunks one after the other (8 rows of 128 bytes, swizzled), so that one
   // TMA box brings whole keys.
   static constexpr int kGroupBytes = CH * 1024;
-  static constexpr int kSoftmaxWarps = 8 * NT;      // two threads a row
+  // Threads a row in the softmax.  Two must exchange their maxima (head dims 64
+  // and 128: a ragged batch 167 us, against 154 with one); the one tile of head
+  // dim 256 needs the eight warps to keep its latencies short.
+  static constexpr int H = D <= 128 ? 1 : 2;
+  static constexpr int kSoftmaxWarps = 4 * H * NT;
   static constexpr int kScoreWarp = kSoftmaxWarps, kValueWarp = kSoftmaxWarps + 1;
   static constexpr int kKeyWarp = kSoftmaxWarps + 2;  // and the one that loads queries and values
   static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
@@ -79,7 +83,8 @@ struct Cfg {
   static_assert(kPCol + T <= kOCol, "tensor memory");
   // shared memory
   static constexpr int kQOff = kSlots * kSlotBytes;
-  // two places a softmax warp for maxima and sums, for the other half of its rows
+  // two places a softmax warp for maxima and sums, for the other half of its
+  // rows (two threads a row)
   static constexpr int kStageOff = kQOff + NT * kQBytes;
   static constexpr int kDescOff = kStageOff + kSoftmaxWarps * 256;
   static constexpr int kBarOff = kDescOff + kDescs * 64;
@@ -638,21 +643,21 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
 }
 
 // ---------------------------------------------------------------------------
-// Softmax warps: two threads share row r of tile t, each with half of a
-// block's keys (and later half of the output's columns).
+// Softmax warps: H threads share row r of tile t, each with its part of a
+// block's keys (and later of the output's columns).
 // ---------------------------------------------------------------------------
 template <int D, bool kBf16>
 __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int t, int half, int warp, int lane) {
   using C = Cfg<D>;
-  constexpr int T = C::T, NT = C::NT, TH = T / 2, DH = D / 2;
+  constexpr int T = C::T, NT = C::NT, H = C::H, TH = T / H, DH = D / H;
   const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
   const Segment *descs = reinterpret_cast<const Segment *>(smem + C::kDescOff);
   const int r = warp * 32 + lane;                        // row of the tile:
   const int r_tok = r / a.G, r_head = r - r_tok * a.G;   // its token and head
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;    // this warp's lanes of tensor memory
   const uint32_t o_addr = tmem + lanes + C::kOCol + t * D + half * DH;
-  uint8_t *stage = smem + C::kStageOff + ((t * 2 + half) * 4 + warp) * 256;
-  const uint8_t *other = smem + C::kStageOff + ((t * 2 + (half ^ 1)) * 4 + warp) * 256;
+  uint8_t *stage = smem + C::kStageOff + ((t * H + half) * 4 + warp) * 256;
+  const uint8_t *other = smem + C::kStageOff + ((t * H + (half ^ (H - 1))) * 4 + warp) * 256;
   const int xchg = C::B_XCHG + t * 4 + warp;
   int x_n = 0;  // exchanges with the warp that has the rows' other halves
   // The issuing warp has negated the scores for a negative scale.  A zero scale
@@ -661,10 +666,14 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
   int seg_n = 0, blk_n = 0;   // segments and score blocks seen
   int slot_n = 1;             // ring slot, of all so far, that holds the current block's values
   auto wait = [&](int bar, int n) { return wait_phase(bars + 8 * bar, n & 1); };
-  // v of the row's other half.  The places alternate: a warp writes one again
-  // only after the exchange in between, which the other warp enters having
-  // read it.
+  // v of the row's other half, if there is one.  The places alternate: a warp
+  // writes one again only after the exchange in between, which the other warp
+  // enters having read it.
   auto exchange = [&](float v, float &v_other) {
+    if constexpr (H == 1) {
+      v_other = v;
+      return true;
+    }
     const int at = (x_n & 1) * 128 + lane * 4;
     *reinterpret_cast<float *>(stage + at) = v;
     __syncwarp();
@@ -744,7 +753,7 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
             const uint32_t v = sbase + sl * C::kSlotBytes;
             const int from = max(st.g0, st.k0 * 16), gap = max(0, st.g1 - from), keys = gap + st.k1 * 16 - st.top;
 #pragma unroll 1
-            for (int i = half * kTileRows + r; i < keys * (D / 8); i += 2 * kTileRows) {
+            for (int i = half * kTileRows + r; i < keys * (D / 8); i += H * kTileRows) {
               const int n = i / (D / 8), c = i % (D / 8), key = n < gap ? from + n : st.top + n - gap;
               asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + (key / 8) * C::kGroupBytes + (c / 8) * 1024 + (key % 8) * 128 + (c % 8) * 16),
                            "r"(0u) : "memory");
@@ -791,6 +800,11 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
       const float base = m == -INFINITY ? 0.f : -m;
       const float2 sc = make_float2(sl2, sl2), bs = make_float2(base, base);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      // Once the product that read the buffer's weights before is done, they go
+      // out 32 at a time, beside the exponentials of the next.
+      if (un > 0 && !wait(C::B_OFULL + u, un - 1)) return false;
+      tc_fence_after();
+      const uint32_t p_addr = tmem + lanes + C::kPCol + u * (T / 2) + half * (TH / 2);
       uint32_t p[TH / 2];
 #pragma unroll
       for (int i = 0; i < TH; i += 2) {
@@ -799,15 +813,10 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
         e.y = ex2(e.y);
         sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
         p[i >> 1] = pack2<kBf16>(e.x, e.y);
+        if (i % 32 == 30) tmem_st16(p_addr + (i >> 1) - 15, p + (i >> 1) - 15);
       }
       sum[0] = add2(sum[0], sum[1]);
       l += sum[0].x + sum[0].y;
-      // the product that read the buffer's weights before is done
-      if (un > 0 && !wait(C::B_OFULL + u, un - 1)) return false;
-      tc_fence_after();
-      const uint32_t p_addr = tmem + lanes + C::kPCol + u * (T / 2) + half * (TH / 2);
-#pragma unroll
-      for (int c = 0; c < TH / 2; c += 16) tmem_st16(p_addr + c, p + c);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -817,7 +826,7 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     // ---- the rows: O / l and LSE ----
     float l_other;
     if (!exchange(l, l_other)) return false;
-    l = half == 0 ? l + l_other : l_other + l;  // the same sum in both halves
+    if (H > 1) l = half == 0 ? l + l_other : l_other + l;  // the same sum in both halves
     const float inv = l == 0.f ? 0.f : rcp(l);
     const int hq = s.h * a.G + r_head, v0 = s.it * NT * a.TQ, tok = v0 + t * a.TQ + r_tok;
     const bool real = r_tok < a.TQ && tok < s.qn;
@@ -842,7 +851,7 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     const int lu = NT == 2 ? t : (blk_n - 1) & 1;  // the last block's values
     if (!wait(C::B_OFULL + lu, NT == 2 ? blk_n - 1 : (blk_n - 1) >> 1)) return false;
     tc_fence_after();
-    // A lane writes its row's half, 32 bytes in a store: whole sectors, without
+    // A lane writes its part of the row, 32 bytes in a store: whole sectors, without
     // a detour through shared memory.  A short loop: code that runs once a unit
     // is fetched anew.
     const bool piece = s.kind != 0;
@@ -891,8 +900,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars + 8 * (C::B_SFULL + i), 1);
-      mbar_init(bars + 8 * (C::B_SFREE + i), 8);  // one arrival a softmax warp of the tile
-      mbar_init(bars + 8 * (C::B_PREADY + i), 8);
+      mbar_init(bars + 8 * (C::B_SFREE + i), 4 * C::H);  // one arrival a softmax warp of the tile
+      mbar_init(bars + 8 * (C::B_PREADY + i), 4 * C::H);
       mbar_init(bars + 8 * (C::B_OFULL + i), 1);
     }
     mbar_init(bars + 8 * C::B_QFULL, 1);
@@ -933,13 +942,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   tmem = __shfl_sync(0xffffffffu, tmem, 0);
   bool ok;
   if (warp >= C::kSoftmaxWarps) {
-    if constexpr (C::NT == 2) regs_dec<64>();  // 96 a thread at launch: 640 x 96 = 512 x 104 + 128 x 64
+    if constexpr (C::NT == 2) regs_dec<72>();  // 168 a thread at launch: 384 x 168 = 256 x 216 + 128 x 72
     if (warp == C::kScoreWarp) ok = issue_scores<D, kBf16>(a, smem, tmem, lane);
     else if (warp == C::kValueWarp) ok = issue_values<D, kBf16>(a, smem, tmem, lane);
     else ok = loader<D>(tm, a, smem, warp != C::kKeyWarp, lane);
   } else {
-    if constexpr (C::NT == 2) regs_inc<104>();
-    ok = softmax<D, kBf16>(a, smem, tmem, warp / 8, (warp / 4) % 2, warp % 4, lane);
+    if constexpr (C::NT == 2) regs_inc<216>();
+    ok = softmax<D, kBf16>(a, smem, tmem, warp / (4 * C::H), (warp / 4) % C::H, warp % 4, lane);
   }
   if (!ok && lane == 0) atomicOr(a.err, kErrWaitFull);  // a wait ran out
   tc_fence_before();
