@@ -9,8 +9,8 @@
 //    and load the packed query rows;
 //  - two issuing warps run S = Q K^T and O += P V on the tensor cores
 //    (tcgen05, accumulators and P in tensor memory);
-//  - softmax warps, one thread per packed query row (two for head dim 256),
-//    turn S into P with a running maximum and sum, and write the rows out.
+//  - softmax warps, one thread per packed query row, turn S into P with a
+//    running maximum and sum, and write the rows out.
 //
 // Units.  The G query heads of one KV head are packed into the rows of a
 // tile, row m = t * G + g, so a KV byte serves all of them: a 128-row tile
@@ -60,11 +60,9 @@ struct Cfg {
   // chunks one after the other (8 rows of 128 bytes, swizzled), so that one
   // TMA box brings whole keys.
   static constexpr int kGroupBytes = CH * 1024;
-  // Threads a row in the softmax.  Two must exchange their maxima (head dims 64
-  // and 128: a ragged batch 167 us, against 154 with one); the one tile of head
-  // dim 256 needs the eight warps to keep its latencies short.
-  static constexpr int H = D <= 128 ? 1 : 2;
-  static constexpr int kSoftmaxWarps = 4 * H * NT;
+  // One thread a row: two would have to exchange their maxima (a ragged batch
+  // of 24 requests took 167 us so, now 154; head dim 256 127 us, now 122).
+  static constexpr int kSoftmaxWarps = 4 * NT;
   static constexpr int kScoreWarp = kSoftmaxWarps, kValueWarp = kSoftmaxWarps + 1;
   static constexpr int kKeyWarp = kSoftmaxWarps + 2;  // and the one that loads queries and values
   static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
@@ -83,18 +81,15 @@ struct Cfg {
   static_assert(kPCol + T <= kOCol, "tensor memory");
   // shared memory
   static constexpr int kQOff = kSlots * kSlotBytes;
-  // two places a softmax warp for maxima and sums, for the other half of its
-  // rows (two threads a row)
-  static constexpr int kStageOff = kQOff + NT * kQBytes;
-  static constexpr int kDescOff = kStageOff + kSoftmaxWarps * 256;
+  static constexpr int kDescOff = kQOff + NT * kQBytes;
   static constexpr int kBarOff = kDescOff + kDescs * 64;
   static constexpr int kSmem = kBarOff + 512;
   // barriers
   static constexpr int B_FULL = 0, B_EMPTY = kSlots, B_SFULL = 2 * kSlots, B_SFREE = B_SFULL + 2;
   static constexpr int B_PREADY = B_SFREE + 2;
   static constexpr int B_OFULL = B_PREADY + 2, B_QFULL = B_OFULL + 2, B_QEMPTY = B_QFULL + 1;
-  static constexpr int B_DFULL = B_QEMPTY + 1, B_DEMPTY = B_DFULL + kDescs, B_XCHG = B_DEMPTY + kDescs;
-  static constexpr int B_COUNT = B_XCHG + 4 * NT;
+  static constexpr int B_DFULL = B_QEMPTY + 1, B_DEMPTY = B_DFULL + kDescs;
+  static constexpr int B_COUNT = B_DEMPTY + kDescs;
   static_assert(B_COUNT * 8 + 16 <= 512 && kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -643,47 +638,24 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
 }
 
 // ---------------------------------------------------------------------------
-// Softmax warps: H threads share row r of tile t, each with its part of a
-// block's keys (and later of the output's columns).
+// Softmax warps: a thread has row r of tile t.
 // ---------------------------------------------------------------------------
 template <int D, bool kBf16>
-__device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int t, int half, int warp, int lane) {
+__device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int t, int warp, int lane) {
   using C = Cfg<D>;
-  constexpr int T = C::T, NT = C::NT, H = C::H, TH = T / H, DH = D / H;
+  constexpr int T = C::T, NT = C::NT;
   const uint32_t sbase = smem_addr(smem), bars = sbase + C::kBarOff;
   const Segment *descs = reinterpret_cast<const Segment *>(smem + C::kDescOff);
   const int r = warp * 32 + lane;                        // row of the tile:
   const int r_tok = r / a.G, r_head = r - r_tok * a.G;   // its token and head
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;    // this warp's lanes of tensor memory
-  const uint32_t o_addr = tmem + lanes + C::kOCol + t * D + half * DH;
-  uint8_t *stage = smem + C::kStageOff + ((t * H + half) * 4 + warp) * 256;
-  const uint8_t *other = smem + C::kStageOff + ((t * H + (half ^ (H - 1))) * 4 + warp) * 256;
-  const int xchg = C::B_XCHG + t * 4 + warp;
-  int x_n = 0;  // exchanges with the warp that has the rows' other halves
+  const uint32_t o_addr = tmem + lanes + C::kOCol + t * D;
   // The issuing warp has negated the scores for a negative scale.  A zero scale
   // becomes one that leaves nothing of a score, since -inf marks a masked one.
   const float sl2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
   int seg_n = 0, blk_n = 0;   // segments and score blocks seen
   int slot_n = 1;             // ring slot, of all so far, that holds the current block's values
   auto wait = [&](int bar, int n) { return wait_phase(bars + 8 * bar, n & 1); };
-  // v of the row's other half, if there is one.  The places alternate: a warp
-  // writes one again only after the exchange in between, which the other warp
-  // enters having read it.
-  auto exchange = [&](float v, float &v_other) {
-    if constexpr (H == 1) {
-      v_other = v;
-      return true;
-    }
-    const int at = (x_n & 1) * 128 + lane * 4;
-    *reinterpret_cast<float *>(stage + at) = v;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bars + 8 * xchg);
-    if (!wait(xchg, x_n)) return false;
-    ++x_n;
-    v_other = *reinterpret_cast<const volatile float *>(other + at);
-    return true;
-  };
-
   for (;;) {
     const int d = seg_n % kDescs;
     if (!wait(C::B_DFULL + d, seg_n / kDescs)) return false;
@@ -724,10 +696,10 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
       if (!wait(C::B_SFULL + u, un)) return false;
       tc_fence_after();
       ++blk_n;
-      const uint32_t s_addr = tmem + lanes + (C::NS == 1 ? 0 : u * T) + half * TH;
-      float x[TH];
+      const uint32_t s_addr = tmem + lanes + (C::NS == 1 ? 0 : u * T);
+      float x[T];
 #pragma unroll
-      for (int c = 0; c < TH; c += 32) tmem_ld32(s_addr + c, reinterpret_cast<uint32_t *>(x + c));
+      for (int c = 0; c < T; c += 32) tmem_ld32(s_addr + c, reinterpret_cast<uint32_t *>(x + c));
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
@@ -736,8 +708,8 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
       if (j0 + T > tile_lim || (j0 < tile_low && j0 + T > a.sinks)) {
         // one bit a key: seen or not; most groups of 32 are seen whole
 #pragma unroll
-        for (int c = 0; c < TH; c += 32) {
-          const int j = j0 + half * TH + c;
+        for (int c = 0; c < T; c += 32) {
+          const int j = j0 + c;
           const uint32_t seen = bits_below(lim - j) & (~bits_below(low - j) | bits_below(a.sinks - j));
           if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
 #pragma unroll
@@ -753,7 +725,7 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
             const uint32_t v = sbase + sl * C::kSlotBytes;
             const int from = max(st.g0, st.k0 * 16), gap = max(0, st.g1 - from), keys = gap + st.k1 * 16 - st.top;
 #pragma unroll 1
-            for (int i = half * kTileRows + r; i < keys * (D / 8); i += H * kTileRows) {
+            for (int i = r; i < keys * (D / 8); i += kTileRows) {
               const int n = i / (D / 8), c = i % (D / 8), key = n < gap ? from + n : st.top + n - gap;
               asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + (key / 8) * C::kGroupBytes + (c / 8) * 1024 + (key % 8) * 128 + (c % 8) * 16),
                            "r"(0u) : "memory");
@@ -766,11 +738,8 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
       slot_n += 2;
       float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int i = 4; i < TH; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], x[i], x[i + 1]);
-      const float mine = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-      float theirs;
-      if (!exchange(mine, theirs)) return false;
-      const float top = fmaxf(mine, theirs) * sl2;
+      for (int i = 4; i < T; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], x[i], x[i + 1]);
+      const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
       // The reference m follows the maximum only once it is 2^8 behind, so
       // the accumulator is hardly ever rescaled; weights stay below 2^8.
       const bool behind = top > m + 8.f || (m == -INFINITY && top > -INFINITY);
@@ -785,7 +754,7 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
           if (!wait(C::B_OFULL + pu, pn)) return false;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < DH; c += 16) {
+          for (int c = 0; c < D; c += 16) {
             float o[16];
             tmem_ld16(o_addr + c, reinterpret_cast<uint32_t *>(o));
             tmem_wait_ld();
@@ -804,10 +773,10 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
       // out 32 at a time, beside the exponentials of the next.
       if (un > 0 && !wait(C::B_OFULL + u, un - 1)) return false;
       tc_fence_after();
-      const uint32_t p_addr = tmem + lanes + C::kPCol + u * (T / 2) + half * (TH / 2);
-      uint32_t p[TH / 2];
+      const uint32_t p_addr = tmem + lanes + C::kPCol + u * (T / 2);
+      uint32_t p[T / 2];
 #pragma unroll
-      for (int i = 0; i < TH; i += 2) {
+      for (int i = 0; i < T; i += 2) {
         float2 e = fma2(make_float2(x[i], x[i + 1]), sc, bs);
         e.x = ex2(e.x);
         e.y = ex2(e.y);
@@ -824,22 +793,19 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     }
 
     // ---- the rows: O / l and LSE ----
-    float l_other;
-    if (!exchange(l, l_other)) return false;
-    if (H > 1) l = half == 0 ? l + l_other : l_other + l;  // the same sum in both halves
     const float inv = l == 0.f ? 0.f : rcp(l);
     const int hq = s.h * a.G + r_head, v0 = s.it * NT * a.TQ, tok = v0 + t * a.TQ + r_tok;
     const bool real = r_tok < a.TQ && tok < s.qn;
     // Where the row goes: row `row` of the output, or of the CTA's piece slot.
     const int row0 = s.kind == 0 ? (s.q0 + tok) * a.Hq + hq
                                  : (blockIdx.x * 2 + (s.kind - 1)) * (NT * kTileRows) + t * kTileRows + r;
-    if (real && half == 0) {
+    if (real) {
       const float lse = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
       if (s.kind != 0) a.lse_part[row0] = lse;
       else if (a.lse != nullptr) a.lse[(size_t)hq * a.total_q + s.q0 + tok] = lse;
     }
     // the head piece's description, for the merge
-    if (s.kind == 1 && t == 0 && half == 0 && r == 0) {
+    if (s.kind == 1 && t == 0 && r == 0) {
       PieceDesc &pd = a.pieces[blockIdx.x];
       pd.q0 = s.q0;
       pd.h = s.h;
@@ -851,30 +817,32 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     const int lu = NT == 2 ? t : (blk_n - 1) & 1;  // the last block's values
     if (!wait(C::B_OFULL + lu, NT == 2 ? blk_n - 1 : (blk_n - 1) >> 1)) return false;
     tc_fence_after();
-    // A lane writes its part of the row, 32 bytes in a store: whole sectors, without
+    // A lane writes its row, 32 bytes in a store: whole sectors, without
     // a detour through shared memory.  A short loop: code that runs once a unit
     // is fetched anew.
     const bool piece = s.kind != 0;
-    uint8_t *dst = piece ? reinterpret_cast<uint8_t *>(a.o_part + (size_t)row0 * D + half * DH)
-                         : static_cast<uint8_t *>(a.out) + ((size_t)row0 * D + half * DH) * 2;
+    uint8_t *dst = piece ? reinterpret_cast<uint8_t *>(a.o_part + (size_t)row0 * D)
+                         : static_cast<uint8_t *>(a.out) + (size_t)row0 * D * 2;
 #pragma unroll 1
-    for (int col = 0; col < DH; col += 32) {
+    for (int col = 0; col < D; col += 32) {
       float o[32];
       tmem_ld32(o_addr + col, reinterpret_cast<uint32_t *>(o));
       tmem_wait_ld();
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;  // no key: O holds nothing to read
-      if (!real) continue;
-      if (piece) {
+      if (real) {
+        if (piece) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) store_sector(dst + (col + i) * 4, reinterpret_cast<const uint32_t *>(o + i), true);
-      } else {
-        uint32_t w[16];
+          for (int i = 0; i < 32; i += 8) store_sector(dst + (col + i) * 4, reinterpret_cast<const uint32_t *>(o + i), true);
+        } else {
+          uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack2<kBf16>(o[2 * i], o[2 * i + 1]);
+          for (int i = 0; i < 16; ++i) w[i] = pack2<kBf16>(o[2 * i], o[2 * i + 1]);
 #pragma unroll
-        for (int i = 0; i < 16; i += 8) store_sector(dst + (col + 2 * i) * 2, w + i, a.wide_out);
+          for (int i = 0; i < 16; i += 8) store_sector(dst + (col + 2 * i) * 2, w + i, a.wide_out);
+        }
       }
+      __syncwarp();  // the next load wants the whole warp
     }
     tc_fence_before();  // the accumulator has been read before this thread's next arrival
     done();
@@ -900,8 +868,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bars + 8 * (C::B_SFULL + i), 1);
-      mbar_init(bars + 8 * (C::B_SFREE + i), 4 * C::H);  // one arrival a softmax warp of the tile
-      mbar_init(bars + 8 * (C::B_PREADY + i), 4 * C::H);
+      mbar_init(bars + 8 * (C::B_SFREE + i), 4);  // one arrival a softmax warp of the tile
+      mbar_init(bars + 8 * (C::B_PREADY + i), 4);
       mbar_init(bars + 8 * (C::B_OFULL + i), 1);
     }
     mbar_init(bars + 8 * C::B_QFULL, 1);
@@ -910,7 +878,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       mbar_init(bars + 8 * (C::B_DFULL + i), 1);
       mbar_init(bars + 8 * (C::B_DEMPTY + i), C::kSoftmaxWarps + 3);
     }
-    for (int i = 0; i < 4 * C::NT; ++i) mbar_init(bars + 8 * (C::B_XCHG + i), 2);
     fence_mbar_init();
   }
   if (warp == C::kScoreWarp) tmem_alloc(tmem_slot, 512);
@@ -948,7 +915,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     else ok = loader<D>(tm, a, smem, warp != C::kKeyWarp, lane);
   } else {
     if constexpr (C::NT == 2) regs_inc<216>();
-    ok = softmax<D, kBf16>(a, smem, tmem, warp / (4 * C::H), (warp / 4) % C::H, warp % 4, lane);
+    ok = softmax<D, kBf16>(a, smem, tmem, warp / 4, warp % 4, lane);
   }
   if (!ok && lane == 0) atomicOr(a.err, kErrWaitFull);  // a wait ran out
   tc_fence_before();
@@ -1144,7 +1111,9 @@ mxa_status_t launch_prefill(const PrefillLaunch &L, cudaStream_t stream) {
 }
 
 namespace {
-constexpr int kUnitCost = 1;
+// Rows out and the next unit's start, in blocks of KV (1: 24 ragged requests
+// 154 us, two windowed prompts 109 us; 3: 150 and 106; 4: 152 and 106).
+constexpr int kUnitCost = 3;
 // Upper bound on the units of one KV head: every row's last group of tiles may be partial.
 long long max_groups(const mxa_decode_params_t &p, int total_q) {
   const int G = p.Hq / p.Hkv, tokens = (p.D <= 128 ? 2 : 1) * (kTileRows / G);
