@@ -70,15 +70,20 @@ struct Cfg {
   static constexpr int kSlots = 128 * 1024 / kSlotBytes;
   static_assert(kSlots % 2 == 0, "keys in the even slots, values in the odd ones");
   static constexpr int kQBytes = kTileRows * D * 2;
-  // Tensor memory: NS score buffers of T columns, two weight buffers of T / 2
-  // (a column holds two weights of a row), then the tiles' accumulators.  Two
-  // tiles' scores take turns in one buffer, which is free again as soon as
-  // they are in registers.  The turns keep the tiles out of step, so that one's
+  // Tensor memory: T columns of scores, two weight buffers of T / 2 (a column
+  // holds two weights of a row), and at the end the tiles' accumulators.  All
+  // scores take turns in one buffer, which is free again as soon as they are
+  // in registers.  The turns keep two tiles out of step, so that one's
   // exponentials run beside the other's loads and stores: with a buffer each
-  // (room for it at D = 64) a block took 3550 cycles instead of 3250.
-  static constexpr int NS = D <= 128 ? 1 : 2;
-  static constexpr int kPCol = NS * T, kOCol = 512 - NT * D;
-  static_assert(kPCol + T <= kOCol, "tensor memory");
+  // (room for it at D = 64) a ragged batch took 161 us instead of 155.
+  static constexpr int kPCol = T, kOCol = 512 - NT * D;
+  // Head dim 256 has room for the queries, packed as the weights are: with the
+  // queries in shared memory 64-key blocks are bound by its bandwidth (a block
+  // moves 192 KB through it, 1536 cycles at 128 bytes each, against 1024 of the
+  // tensor cores; 128 KB so).
+  static constexpr bool kQTmem = D == 256;
+  static constexpr int kQCol = kPCol + T;
+  static_assert(kQCol + (kQTmem ? D / 2 : 0) <= kOCol, "tensor memory");
   // shared memory
   static constexpr int kQOff = kSlots * kSlotBytes;
   static constexpr int kDescOff = kQOff + NT * kQBytes;
@@ -89,7 +94,8 @@ struct Cfg {
   static constexpr int B_PREADY = B_SFREE + 2;
   static constexpr int B_OFULL = B_PREADY + 2, B_QFULL = B_OFULL + 2, B_QEMPTY = B_QFULL + 1;
   static constexpr int B_DFULL = B_QEMPTY + 1, B_DEMPTY = B_DFULL + kDescs;
-  static constexpr int B_COUNT = B_DEMPTY + kDescs;
+  static constexpr int B_QREADY = B_DEMPTY + kDescs;  // the queries are in tensor memory
+  static constexpr int B_COUNT = B_QREADY + 1;
   static_assert(B_COUNT * 8 + 16 <= 512 && kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -540,24 +546,27 @@ __device__ bool issue_scores(const PrefillArgs &a, uint8_t *smem, uint32_t tmem,
   for (int seg_n = 0;; ++seg_n) {
     if (!take_segment<D>(a, smem, seg_n, lane, w)) return false;
     if (w.kind < 0) return true;
-    if (!wait(C::B_QFULL, seg_n)) return false;
+    if (!wait(C::kQTmem ? C::B_QREADY : C::B_QFULL, seg_n)) return false;
+    if (C::kQTmem) tc_fence_after();
     for (int j = 0; j < w.n; ++j) {
       if (!wait(C::B_FULL + slot, phase)) return false;
       const uint32_t k = smem_desc_lo(sbase + slot * C::kSlotBytes, 16);
       for (int t = 0; t < w.tiles; ++t) {
         const int i = NT == 2 ? t : (s_n[0] + s_n[1]) & 1;
-        const int before = C::NS == 1 ? last : i;
-        if (s_n[before] > 0 && !wait(C::B_SFREE + before, s_n[before] - 1)) return false;
+        if (s_n[last] > 0 && !wait(C::B_SFREE + last, s_n[last] - 1)) return false;
         tc_fence_after();
-        const uint32_t q = q_lo + t * (C::kQBytes / 16), d = tmem + (C::NS == 1 ? 0 : i * T);
+        const uint32_t q = q_lo + t * (C::kQBytes / 16);
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss<kHi, kHiKV>(d, q + (kk / 4) * (kTileRows * 8) + (kk % 4) * 2, k + (kk / 4) * 64 + (kk % 4) * 2, idesc, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t kd = k + (kk / 4) * 64 + (kk % 4) * 2;
+            if constexpr (C::kQTmem) mma_ts<kHiKV>(tmem, tmem + C::kQCol + kk * 8, kd, idesc, kk > 0);
+            else mma_ss<kHi, kHiKV>(tmem, q + (kk / 4) * (kTileRows * 8) + (kk % 4) * 2, kd, idesc, kk > 0);
+          }
           mma_commit(bars + 8 * (C::B_SFULL + i));
           if (t + 1 == w.tiles) {
             mma_commit(bars + 8 * (C::B_EMPTY + slot));
-            if (j + 1 == w.n) mma_commit(bars + 8 * C::B_QEMPTY);
+            if (!C::kQTmem && j + 1 == w.n) mma_commit(bars + 8 * C::B_QEMPTY);
           }
         }
         __syncwarp();
@@ -689,6 +698,29 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     const int tile_lim = a.causal ? L - qn + tt0 + 1 : L;
     const int tile_low = a.window > 0 ? L - qn + min(tt0 + a.TQ, qn) - a.window : 0;
 
+    if constexpr (C::kQTmem) {
+      // This row's queries go to tensor memory; the scores of the unit before
+      // have been seen, so its queries are done with.
+      if (!wait(C::B_QFULL, seg_n)) return false;
+#pragma unroll 1
+      for (int ch = 0; ch < C::CH; ++ch) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4 *>(w + 4 * i) =
+              *reinterpret_cast<const uint4 *>(smem + C::kQOff + ch * (kTileRows * 128) + r * 128 + ((i ^ (r & 7)) << 4));
+        tmem_st16(tmem + lanes + C::kQCol + ch * 32, w);
+        tmem_st16(tmem + lanes + C::kQCol + ch * 32 + 16, w + 16);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bars + 8 * C::B_QREADY);
+        mbar_arrive(bars + 8 * C::B_QEMPTY);
+      }
+    }
+
     float m = -INFINITY, l = 0.f;  // running maximum (base 2, scaled) and sum
     for (int blk = blk_beg; blk < blk_end; ++blk) {
       // barriers: the tile's, or with one tile those of the block's parity
@@ -696,7 +728,7 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
       if (!wait(C::B_SFULL + u, un)) return false;
       tc_fence_after();
       ++blk_n;
-      const uint32_t s_addr = tmem + lanes + (C::NS == 1 ? 0 : u * T);
+      const uint32_t s_addr = tmem + lanes;
       float x[T];
 #pragma unroll
       for (int c = 0; c < T; c += 32) tmem_ld32(s_addr + c, reinterpret_cast<uint32_t *>(x + c));
@@ -873,7 +905,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       mbar_init(bars + 8 * (C::B_OFULL + i), 1);
     }
     mbar_init(bars + 8 * C::B_QFULL, 1);
-    mbar_init(bars + 8 * C::B_QEMPTY, 1);
+    mbar_init(bars + 8 * C::B_QEMPTY, C::kQTmem ? 4 : 1);
+    mbar_init(bars + 8 * C::B_QREADY, 4);
     for (int i = 0; i < kDescs; ++i) {
       mbar_init(bars + 8 * (C::B_DFULL + i), 1);
       mbar_init(bars + 8 * (C::B_DEMPTY + i), C::kSoftmaxWarps + 3);
