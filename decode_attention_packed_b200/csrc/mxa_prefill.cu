@@ -960,12 +960,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 // ---------------------------------------------------------------------------
 // Merge of the units that ranges cut: cut i (between CTAs i - 1 and i) of a
 // unit with n pieces takes the (i - c_first)-th share of its rows, and
-// blockIdx.y a part of that: two rows a warp where a unit has two pieces, since
-// a row is a chain of a few dependent loads (with a quarter of the warps the
-// merge took 20 us of a 240 us call, now under 5).
+// blockIdx.y a part of that: four rows a warp where a unit has two pieces.  A
+// row is a chain of a few dependent loads, and the pieces of a full grid are 38
+// MB at D = 128, read from L2: with two rows of up to kFewPieces pieces on
+// their way at once two windowed prompts take 104 us, one row after the other
+// 110.  Merging in the attention kernel, by the last piece to arrive, was
+// slower (114 us: a few warps wait where this kernel has them by the hundred).
 //   LSE = ln sum_p exp(lse_p),   O = sum_p exp(lse_p - LSE) O_p
 // ---------------------------------------------------------------------------
-constexpr int kMergeThreads = 256, kMergeParts = 16;
+constexpr int kMergeThreads = 128, kMergeParts = 16, kFewPieces = 3;
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ PrefillArgs a) {
   constexpr int NT = Cfg<D>::NT;
@@ -983,6 +986,56 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
   const int part = ((cta - pd.c_first - 1) * gridDim.y + blockIdx.y) * kWarps + (threadIdx.x >> 5);
   const int beg = (int)((long long)rows * part / parts), end = (int)((long long)rows * (part + 1) / parts);
   auto slot_of = [&](int i) -> size_t { return i == 0 ? (size_t)pd.c_first * 2 + 1 : (size_t)(pd.c_first + i) * 2; };
+  if (n <= kFewPieces) {
+    // two rows at once, every load on its way before the first is used
+    for (int m = beg; m < end; m += 2) {
+      float lp[2][kFewPieces], lse2[2];
+      float4 v[2][kFewPieces][D > 128 ? 2 : 1];
+      size_t at[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int mi = min(m + i, end - 1), tok = mi / a.G, g = mi - tok * a.G;
+        const int row = (tok / a.TQ) * kTileRows + (tok % a.TQ) * a.G + g;
+        at[i] = (size_t)(pd.q0 + pd.t0 + tok) * a.Hq + pd.h * a.G + g;
+#pragma unroll
+        for (int p = 0; p < kFewPieces; ++p) {
+          const size_t pr = slot_of(min(p, n - 1)) * (NT * kTileRows) + row;
+          lp[i][p] = p < n ? a.lse_part[pr] * kLog2e : -INFINITY;
+#pragma unroll
+          for (int k = 0; k < (D > 128 ? 2 : 1); ++k)
+            v[i][p][k] = p < n && lane * 4 < D ? *reinterpret_cast<const float4 *>(a.o_part + pr * D + k * 128 + lane * 4)
+                                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (m + i >= end) break;
+        float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int p = 0; p < kFewPieces; ++p) mx = fmaxf(mx, lp[i][p]);
+        if (mx == -INFINITY) mx = 0.f;  // no piece saw a key, or all hold NaN, which stays
+#pragma unroll
+        for (int p = 0; p < kFewPieces; ++p) sum += ex2(lp[i][p] - mx);
+        lse2[i] = sum == 0.f ? -INFINITY : mx + log2f(sum);
+        if (lane == 0 && a.lse != nullptr)
+          a.lse[(at[i] % a.Hq) * a.total_q + at[i] / a.Hq] = lse2[i] * kLn2;
+#pragma unroll
+        for (int k = 0; k < (D > 128 ? 2 : 1); ++k) {
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int p = 0; p < kFewPieces; ++p) {
+            const float wgt = lp[i][p] == -INFINITY ? 0.f : ex2(lp[i][p] - lse2[i]);
+            acc.x += wgt * v[i][p][k].x; acc.y += wgt * v[i][p][k].y;
+            acc.z += wgt * v[i][p][k].z; acc.w += wgt * v[i][p][k].w;
+          }
+          if (lane * 4 < D)
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at[i] * D + k * 128 + lane * 4) =
+                make_uint2(pack2<kBf16>(acc.x, acc.y), pack2<kBf16>(acc.z, acc.w));
+        }
+      }
+    }
+    return;
+  }
   for (int m = beg; m < end; ++m) {
     const int tok = m / a.G, g = m % a.G;
     const int row = (tok / a.TQ) * kTileRows + (tok % a.TQ) * a.G + g;  // of the unit's tiles
@@ -991,8 +1044,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     float sum = 0.f;
-    if (mx != -INFINITY)
-      for (int p = lane; p < n; p += 32) sum += ex2(a.lse_part[slot_of(p) * (NT * kTileRows) + row] * kLog2e - mx);
+    if (mx == -INFINITY) mx = 0.f;
+    for (int p = lane; p < n; p += 32) sum += ex2(a.lse_part[slot_of(p) * (NT * kTileRows) + row] * kLog2e - mx);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum);  // NaN stays
@@ -1004,7 +1057,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
       for (int p = 0; p < n; ++p) {
         const size_t pr = slot_of(p) * (NT * kTileRows) + row;
         const float lp = a.lse_part[pr];
-        const float wgt = lp == -INFINITY || lse2 == -INFINITY ? 0.f : ex2(lp * kLog2e - lse2);
+        const float wgt = lp == -INFINITY ? 0.f : ex2(lp * kLog2e - lse2);
         const float4 v = *reinterpret_cast<const float4 *>(a.o_part + pr * D + c);
         acc.x += wgt * v.x; acc.y += wgt * v.y; acc.z += wgt * v.z; acc.w += wgt * v.w;
       }
