@@ -337,3 +337,26 @@ def test_a_stream_given_by_hand():
         torch.empty(64 << 20, dtype=torch.uint8, device="cuda").fill_(255)  # what the current stream allocates meanwhile
         torch.cuda.synchronize()
         assert torch.equal(out.cpu().view(torch.int16), first[0].view(torch.int16)) and torch.equal(lse.cpu(), first[1])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_output_at_a_multiple_of_16_bytes(D):
+    inp, q, cu = draw([130, 1, 40], [700, 200, 2000], D=D, seed=1960)
+    out = torch.empty(q.numel() + 8, dtype=q.dtype, device="cuda")[8:].view(q.shape)
+    assert out.data_ptr() % 32 == 16
+    check(inp, q, cu, *run(inp, q, cu, out=out))
+
+
+@pytest.mark.parametrize("q_lens,lengths", [([300, 2], [3000, 900]), ([1], [9000])])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_nan_in_seen_places_stays(q_lens, lengths, D):
+    # also through the merge of units cut in few and in many pieces
+    inp, q, cu = draw(q_lens, lengths, D=D, seed=1970)
+    keep = inp.v_cache.clone()
+    inp.v_cache.fill_(float("nan"))
+    out, lse = run(inp, q, cu)
+    assert out.isnan().all() and lse.isfinite().all()
+    inp.v_cache.copy_(keep)
+    inp.k_cache.fill_(float("nan"))
+    out, lse = run(inp, q, cu)
+    assert out.isnan().all() and lse.isnan().all()
