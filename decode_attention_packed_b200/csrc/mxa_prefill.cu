@@ -17,8 +17,8 @@
 // holds floor(128 / G) tokens.  A unit is (batch row, KV head, group of
 // tiles): two tiles for head dims 64 and 128 (while one tile's scores are in
 // the softmax, the tensor cores work on the other's), one for 256, whose
-// accumulator fills half of tensor memory (two score buffers take the
-// second tile's place).
+// accumulator fills half of tensor memory (its queries take the second
+// tile's place).
 //
 // Split.  All units, each a fixed cost plus its visible KV blocks, are laid
 // end to end and cut into equal contiguous ranges, one per CTA: ragged
@@ -28,15 +28,17 @@
 //
 // What bounds it (B200, per pair of tiles and 128 keys).  D = 128: the tensor
 // cores 2048 cycles (four products of 512), the exponentials 2048 (16 a cycle
-// and SM, both tiles' 32768).  D = 64: 1024 and 2048.  Measured: about 3000 to
-// 3100 in either case, since a tile's loads, maximum, hand-overs and stores are
-// only partly hidden behind the other tile's exponentials; 4096 tokens after
-// 12288 keys (64 query heads, 8 KV heads, D = 128) run at 1260 TFLOP/s for a
-// millisecond or two and at about 1050 when the card's power limit holds the
-// clock.  Tried and not kept: computing part of the exponentials with a
-// polynomial on the floating-point pipe (an eighth: no change; a quarter:
-// slower), turns of the two tiles at the exponentials (no change), handing the
-// weights over in two parts (slower), a fifth ring slot (no change).
+// and SM, both tiles' 32768), shared memory 2048 (256 KB at 128 bytes a cycle:
+// operands and loads).  D = 64: 1024, 2048 and 1024.  Measured: 2600 to 2700 in
+// either case, since a tile's loads, maximum, hand-overs and stores are only
+// partly hidden behind the other tile's exponentials; 4096 tokens after 12288
+// keys (64 query heads, 8 KV heads, D = 128) run at 1400 TFLOP/s for a
+// millisecond or two and at about 1200 when the card's power limit holds the
+// clock.  D = 256, per tile and 64 keys: the tensor cores 1024, measured 1800,
+// one tile's hand-overs with nothing beside them.  Tried and not kept: turns of
+// the two tiles at the exponentials, a block's scores on their way during the
+// hand-over of the weights before (slower), two groups of softmax warps that
+// take the blocks of D = 256 in turn (no change).
 #include "mxa_config.h"
 #include "mxa_device.cuh"
 #include "mxa_launch.h"
