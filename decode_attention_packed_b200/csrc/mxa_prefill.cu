@@ -366,7 +366,7 @@ __device__ bool loader(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *sme
   const int pages = T / ps, rest = T % ps;  // a block's length in pages
   const bool has_box = lane < T / bt;       // this lane has box `lane` of a block
   int slot = values ? 1 : 0, phase = 1;     // ring slot of the next block, and the phase that frees it
-  int loaded = 0, seg_n = 0;
+  int loaded = 0, asked = 0, seg_n = 0;     // blocks and units' queries on their way
   bool ok = true, bad_page = false;
   auto page_of = [&](int b, int p) { return has_box && p < a.mpps ? a.block_table[(size_t)b * a.mpps + p] : -1; };
   for (;; ++seg_n) {
@@ -411,6 +411,7 @@ __device__ bool loader(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *sme
         tma_load_3d(sbase + C::kQOff + t * C::kQBytes + ch * (kTileRows * 128), &tm.q, ch * 64, s.h * a.G,
                     s.q0 + t0 + t * a.TQ, bars + 8 * C::B_QFULL);
       }
+      ++asked;
     }
     for (int blk = s.beg; blk < s.end; ++blk) {
       const int tok0 = span.block(blk) * T, tok = tok0 + lane * bt;
@@ -467,7 +468,7 @@ __device__ bool loader(const PrefillMaps &tm, const PrefillArgs &a, uint8_t *sme
   // Leave only when the copies issued here have landed.
   for (int j = max(0, loaded - C::kSlots / 2); j < loaded; ++j)
     ok &= wait_phase(bars + 8 * (C::B_FULL + 2 * (j % (C::kSlots / 2)) + (values ? 1 : 0)), (j / (C::kSlots / 2)) & 1);
-  if (values && seg_n > 0) ok &= wait_phase(bars + 8 * C::B_QFULL, (seg_n - 1) & 1);
+  if (asked > 0) ok &= wait_phase(bars + 8 * C::B_QFULL, (asked - 1) & 1);
   return ok;
 }
 
