@@ -125,15 +125,17 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-# The current stream's handle without a Stream object around it, which costs
-# more host time than the rest of a short call's marshalling.
+# The current stream's handle without a Stream object around it, and the
+# current device without the look at torch's initialisation before it: they
+# cost more host time than the rest of a short call's marshalling.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -473,7 +475,7 @@ def prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, ma
         prepared = prepare_prefill(q, cu_seqlens_q, k_cache, block_table, max_seqlen_q=max_seqlen_q,
                                    max_seqlen_k=max_seqlen_k)
         _lend(prepared.workspace, stream)
-    p, dev, dtype = prepared.params, torch.cuda.current_device(), q.dtype
+    p, dev, dtype = prepared.params, _current_device(), q.dtype
     B = p.B
     if dtype is not (torch.bfloat16 if p.dtype == MXA_BF16 else torch.float16):
         raise TypeError("q must have the type that the call was prepared for")
@@ -510,10 +512,10 @@ def _want(device: int, t: torch.Tensor, name: str, dtype, shape=None) -> None:
     current one, or an error that names it."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
     if t.get_device() != device:  # -1 for a tensor on the host
         raise ValueError(f"{name} must be on the current CUDA device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
 
@@ -530,7 +532,7 @@ def extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, *, page_
     behind the last row are padding with slot -1.  A row whose pages do not fit
     its table or the free list takes none: its slots are -1 and its length is
     unchanged."""
-    dev, int32 = torch.cuda.current_device(), torch.int32
+    dev, int32 = _current_device(), torch.int32
     _want(dev, block_table, "block_table", int32)
     B = block_table.shape[0]
     _want(dev, cache_seqlens, "cache_seqlens", int32, (B,))
@@ -559,7 +561,7 @@ def write_cache(k_new, v_new, k_cache, v_cache, slots, *, stream=None) -> None:
     """Copy k_new / v_new [total, Hkv, D] into the cache slots of
     extend_tables.  The tokens may be strided (slices of one fused
     projection); a token with slot -1 is left out; slots are distinct."""
-    dev, dtype = torch.cuda.current_device(), k_cache.dtype
+    dev, dtype = _current_device(), k_cache.dtype
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise TypeError("the cache must be float16 or bfloat16")
     _want(dev, k_cache, "k_cache", dtype)
