@@ -21,12 +21,12 @@ namespace {
 //
 // A few bytes a row and a token: the call is bound by launch and load
 // latency (64 rows of one token, or 8192 tokens of 300 rows: 4.5 us on the
-// device, 14 us a call from Python).  One launch: every CTA scans the rows itself (chunks of kRows rows
-// in shared memory with a carry, so any number of rows works; the offsets and
-// lengths are 8 bytes a row and come from L2) and then serves its share of
-// the pages and tokens of the chunk, found by binary search.  A page taken in
-// this call is read from the free list, never from the table, so no CTA
-// reads what another one writes.
+// device, 13 us a call from Python).  One launch: every CTA scans the rows
+// itself (chunks of kRows rows in shared memory with a carry, so any number of
+// rows works; the offsets and lengths are 8 bytes a row and come from L2) and
+// then serves its share of the pages and tokens of the chunk, found by binary
+// search.  A page taken in this call is read from the free list, never from
+// the table, so no CTA reads what another one writes.
 // ---------------------------------------------------------------------------
 constexpr int kTableThreads = 256;
 constexpr int kRowsPerThread = 4;
