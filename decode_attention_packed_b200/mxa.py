@@ -140,6 +140,23 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(stream, shape, dtype, device) -> torch.Tensor:
+    """torch.empty for a call on `stream` (None: the current one).  The memory
+    comes from the pool of the stream that writes it, so nothing queued on the
+    current stream still uses it and nothing allocated there gets it while the
+    call runs.  It is lent to the current stream, where the caller waits for
+    the call and reads it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)  # 0 and 1 name the legacy default stream
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 # --------------------------------------------------------------------------
 # the C calls, same names
 # --------------------------------------------------------------------------
@@ -351,13 +368,15 @@ class Prepared:
 
 
 def prepare(q, k_cache, block_table, *, max_seqlen_k=None, num_splits=0, plan=None,
-            device=None, window=0, sinks=0) -> Prepared:
+            device=None, window=0, sinks=0, stream=None) -> Prepared:
+    """The plan and the workspace of decode calls, for a serving loop to keep:
+    calls on `stream` (None: the current one)."""
     params = params_for(q, k_cache, block_table, max_seqlen_k)
     if plan is None:
         plan = mxa_plan_window(params, window, sinks, num_splits) if window else mxa_plan(params, num_splits)
     ws = None
     if plan.workspace_bytes:
-        ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=device or q.device)
+        ws = _empty(stream, plan.workspace_bytes, torch.uint8, device or q.device)
     return Prepared(params, plan, ws)
 
 
@@ -383,14 +402,13 @@ def decode(q, k_cache, v_cache, block_table, cache_seqlens, *, scale=None, causa
         scale = q.shape[-1] ** -0.5
     if prepared is None:
         prepared = prepare(q, k_cache, block_table, max_seqlen_k=max_seqlen_k, num_splits=num_splits,
-                           window=window, sinks=sinks)
-        _lend(prepared.workspace, stream)
+                           window=window, sinks=sinks, stream=stream)
     f32 = out_dtype == torch.float32 or (out is not None and out.dtype == torch.float32)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=q.device) if f32 else torch.empty_like(q)
+        out = _empty(stream, q.shape, torch.float32 if f32 else q.dtype, q.device)
     if lse is None and return_lse:
         B, q_len, Hq, _ = q.shape
-        lse = torch.empty((B, Hq, q_len), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (B, Hq, q_len), torch.float32, q.device)
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new go together")
     if f32:
@@ -429,12 +447,12 @@ def decode_varlen(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens,
         plan = mxa_plan(params, num_splits)
         ws = None
         if plan.workspace_bytes:
-            ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device)
+            ws = _empty(stream, plan.workspace_bytes, torch.uint8, q.device)
         prepared = Prepared(params, plan, ws)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(stream, q.shape, q.dtype, q.device)
     if lse is None and return_lse:
-        lse = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (Hq, total_q), torch.float32, q.device)
     mxa_decode_fwd_varlen(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, prepared.params,
                           scale, causal, prepared.plan, prepared.workspace, out, lse, stream)
     return out, lse
@@ -444,9 +462,10 @@ def decode_varlen(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens,
 # chunks of new tokens, and the cache's bookkeeping
 # --------------------------------------------------------------------------
 
-def prepare_prefill(q, cu_seqlens_q, k_cache, block_table, *, max_seqlen_q, max_seqlen_k=None) -> Prepared:
+def prepare_prefill(q, cu_seqlens_q, k_cache, block_table, *, max_seqlen_q, max_seqlen_k=None,
+                    stream=None) -> Prepared:
     """The workspace of prefill calls with up to q.shape[0] packed tokens, for
-    a serving loop to keep."""
+    a serving loop to keep: calls on `stream` (None: the current one)."""
     total_q, Hq, D = q.shape
     B = cu_seqlens_q.shape[0] - 1
     shape = torch.empty((B, int(max_seqlen_q), Hq, D), dtype=q.dtype, device="meta")
@@ -454,7 +473,7 @@ def prepare_prefill(q, cu_seqlens_q, k_cache, block_table, *, max_seqlen_q, max_
     size = mxa_prefill_workspace_size(params, total_q)
     if size == SIZE_MAX:  # the run call names the reason
         size = 0
-    return Prepared(params, None, torch.empty(size, dtype=torch.uint8, device=q.device))
+    return Prepared(params, None, _empty(stream, size, torch.uint8, q.device))
 
 
 def prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, max_seqlen_q, scale=None, causal=True,
@@ -473,8 +492,7 @@ def prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, ma
         scale = q.shape[-1] ** -0.5
     if prepared is None:
         prepared = prepare_prefill(q, cu_seqlens_q, k_cache, block_table, max_seqlen_q=max_seqlen_q,
-                                   max_seqlen_k=max_seqlen_k)
-        _lend(prepared.workspace, stream)
+                                   max_seqlen_k=max_seqlen_k, stream=stream)
     p, dev, dtype = prepared.params, _current_device(), q.dtype
     B = p.B
     if dtype is not (torch.bfloat16 if p.dtype == MXA_BF16 else torch.float16):
@@ -488,23 +506,16 @@ def prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, ma
     if block_table is not None:
         _want(dev, block_table, "block_table", torch.int32, (B, p.max_pages_per_seq))
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(stream, q.shape, dtype, q.device)
     else:
         _want(dev, out, "out", dtype, q.shape)
     if lse is None and return_lse:
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (q.shape[1], q.shape[0]), torch.float32, q.device)
     elif lse is not None:
         _want(dev, lse, "lse", torch.float32, (q.shape[1], q.shape[0]))
     mxa_prefill_fwd(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, p, scale, causal,
                     window, sinks, prepared.workspace, out, lse, stream)
     return out, lse
-
-
-def _lend(workspace: Optional[torch.Tensor], stream) -> None:
-    """Keep a call's own workspace from being handed out again while `stream`
-    (None: the current one, whose order keeps it) still uses it."""
-    if workspace is not None and stream is not None:
-        workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
 def _want(device: int, t: torch.Tensor, name: str, dtype, shape=None) -> None:
@@ -539,15 +550,15 @@ def extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, *, page_
     _want(dev, cu_seqlens_q, "cu_seqlens_q", int32, (B + 1,))
     _want(dev, free_pages, "free_pages", int32)
     if slots is None:
-        slots = torch.empty(total_q, dtype=int32, device=block_table.device)
+        slots = _empty(stream, total_q, int32, block_table.device)
     else:
         _want(dev, slots, "slots", int32, (total_q,))
     if new_seqlens is None:
-        new_seqlens = torch.empty_like(cache_seqlens)
+        new_seqlens = _empty(stream, (B,), int32, block_table.device)
     else:
         _want(dev, new_seqlens, "new_seqlens", int32, (B,))
     if pages_used is None:
-        pages_used = torch.empty(1, dtype=int32, device=block_table.device)
+        pages_used = _empty(stream, 1, int32, block_table.device)
     else:
         _want(dev, pages_used, "pages_used", int32, (1,))
     if B and new_seqlens.data_ptr() == cache_seqlens.data_ptr():
