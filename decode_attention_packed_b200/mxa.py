@@ -367,6 +367,21 @@ class Prepared:
     workspace: Optional[torch.Tensor]
 
 
+def _widened(params: mxa_decode_params_t, max_seqlen_q, max_seqlen_k) -> mxa_decode_params_t:
+    """The prepared shape with this call's bounds (None: none stated) where
+    they go further, up to what a row of the cache holds; the library then
+    checks that plan and workspace still do."""
+    q_len = params.q_len if max_seqlen_q is None else max(params.q_len, int(max_seqlen_q))
+    k_len = params.max_seqlen_k
+    if max_seqlen_k is not None and max_seqlen_k > k_len:
+        k_len = max(k_len, min(int(max_seqlen_k), params.max_pages_per_seq * params.page_size))
+    if q_len == params.q_len and k_len == params.max_seqlen_k:
+        return params
+    wide = mxa_decode_params_t.from_buffer_copy(params)
+    wide.q_len, wide.max_seqlen_k = q_len, k_len
+    return wide
+
+
 def prepare(q, k_cache, block_table, *, max_seqlen_k=None, num_splits=0, plan=None,
             device=None, window=0, sinks=0, stream=None) -> Prepared:
     """The plan and the workspace of decode calls, for a serving loop to keep:
@@ -403,6 +418,7 @@ def decode(q, k_cache, v_cache, block_table, cache_seqlens, *, scale=None, causa
     if prepared is None:
         prepared = prepare(q, k_cache, block_table, max_seqlen_k=max_seqlen_k, num_splits=num_splits,
                            window=window, sinks=sinks, stream=stream)
+    params = _widened(prepared.params, None, max_seqlen_k)
     f32 = out_dtype == torch.float32 or (out is not None and out.dtype == torch.float32)
     if out is None:
         out = _empty(stream, q.shape, torch.float32 if f32 else q.dtype, q.device)
@@ -416,16 +432,16 @@ def decode(q, k_cache, v_cache, block_table, cache_seqlens, *, scale=None, causa
             raise ValueError("a float32 output is not offered with a window")
         if k_new is not None:
             raise ValueError("a float32 output is not offered with k_new / v_new")
-        mxa_decode_fwd_f32out(q, k_cache, v_cache, block_table, cache_seqlens, prepared.params, scale, causal,
+        mxa_decode_fwd_f32out(q, k_cache, v_cache, block_table, cache_seqlens, params, scale, causal,
                               prepared.plan, prepared.workspace, out, lse, stream)
     elif window:
-        mxa_decode_fwd_window(q, k_cache, v_cache, k_new, v_new, block_table, cache_seqlens, prepared.params, scale,
+        mxa_decode_fwd_window(q, k_cache, v_cache, k_new, v_new, block_table, cache_seqlens, params, scale,
                               window, sinks, prepared.plan, prepared.workspace, out, lse, stream)
     elif k_new is None:
-        mxa_decode_fwd_with_plan(q, k_cache, v_cache, block_table, cache_seqlens, prepared.params, scale,
+        mxa_decode_fwd_with_plan(q, k_cache, v_cache, block_table, cache_seqlens, params, scale,
                                  causal, prepared.plan, prepared.workspace, out, lse, stream)
     else:
-        mxa_decode_fwd_append(q, k_cache, v_cache, k_new, v_new, block_table, cache_seqlens, prepared.params,
+        mxa_decode_fwd_append(q, k_cache, v_cache, k_new, v_new, block_table, cache_seqlens, params,
                               scale, causal, prepared.plan, prepared.workspace, out, lse, stream)
     return out, lse
 
@@ -449,11 +465,12 @@ def decode_varlen(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens,
         if plan.workspace_bytes:
             ws = _empty(stream, plan.workspace_bytes, torch.uint8, q.device)
         prepared = Prepared(params, plan, ws)
+    params = _widened(prepared.params, max_seqlen_q, max_seqlen_k)
     if out is None:
         out = _empty(stream, q.shape, q.dtype, q.device)
     if lse is None and return_lse:
         lse = _empty(stream, (Hq, total_q), torch.float32, q.device)
-    mxa_decode_fwd_varlen(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, prepared.params,
+    mxa_decode_fwd_varlen(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, params,
                           scale, causal, prepared.plan, prepared.workspace, out, lse, stream)
     return out, lse
 
@@ -493,7 +510,7 @@ def prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, ma
     if prepared is None:
         prepared = prepare_prefill(q, cu_seqlens_q, k_cache, block_table, max_seqlen_q=max_seqlen_q,
                                    max_seqlen_k=max_seqlen_k, stream=stream)
-    p, dev, dtype = prepared.params, _current_device(), q.dtype
+    p, dev, dtype = _widened(prepared.params, max_seqlen_q, max_seqlen_k), _current_device(), q.dtype
     B = p.B
     if dtype is not (torch.bfloat16 if p.dtype == MXA_BF16 else torch.float16):
         raise TypeError("q must have the type that the call was prepared for")

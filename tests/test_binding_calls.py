@@ -1,0 +1,93 @@
+"""What the binding hands to the library, and what it refuses before it: on the
+CPU, with the library's run entry points replaced by a record of their
+arguments and host tensors in the place of the device's."""
+import ctypes
+
+import pytest
+import torch
+
+from decode_attention_packed_b200 import mxa
+
+RUNS = ("mxa_decode_fwd_with_plan", "mxa_decode_fwd_window", "mxa_decode_fwd_f32out", "mxa_decode_fwd_varlen",
+        "mxa_decode_fwd_append", "mxa_prefill_fwd", "mxa_extend_tables", "mxa_cache_write")
+B, HQ, HKV, D, PAGE, WIDTH = 3, 8, 2, 64, 16, 64
+
+
+@pytest.fixture
+def ran(monkeypatch):
+    """The run calls so far: (entry point, its arguments, its params or None)."""
+    calls = []
+    monkeypatch.setattr(mxa, "_current_device", lambda: -1)  # where host tensors say they are
+    monkeypatch.setattr(mxa, "_raw_stream", lambda device: 0)
+    plan, plan_window = mxa.mxa_plan, mxa.mxa_plan_window
+    monkeypatch.setattr(mxa, "mxa_plan", lambda p, splits=0: plan(p, splits, 148))
+    monkeypatch.setattr(mxa, "mxa_plan_window", lambda p, w, s, splits=0: plan_window(p, w, s, splits, 148))
+    monkeypatch.setattr(mxa._lib, "mxa_prefill_workspace_size", lambda *args: 4096)
+
+    def entry(name):
+        def run(*args):
+            p = [a._obj for a in args if isinstance(getattr(a, "_obj", None), mxa.mxa_decode_params_t)]
+            shape = mxa.mxa_decode_params_t.from_buffer_copy(p[0]) if p else None
+            calls.append((name, args, shape))
+            return mxa.MXA_OK
+        return run
+
+    for name in RUNS:
+        monkeypatch.setattr(mxa._lib, name, entry(name))
+    return calls
+
+
+def tensors(q_tokens=B):
+    return dict(q=torch.zeros(q_tokens, HQ, D, dtype=torch.float16),
+                k=torch.zeros(B * WIDTH, PAGE, HKV, D, dtype=torch.float16),
+                v=torch.zeros(B * WIDTH, PAGE, HKV, D, dtype=torch.float16),
+                table=torch.arange(B * WIDTH, dtype=torch.int32).view(B, WIDTH),
+                lens=torch.full((B,), 500, dtype=torch.int32), cu=torch.arange(B + 1, dtype=torch.int32))
+
+
+def bounds_call(which, t, prepared_q, prepared_k):
+    """A call of `which` whose preparation had the given bounds, and that takes its own as keywords."""
+    row_q = t["q"].view(B, 1, HQ, D)
+    if which == "prefill":
+        prep = mxa.prepare_prefill(t["q"], t["cu"], t["k"], t["table"], max_seqlen_q=prepared_q, max_seqlen_k=prepared_k)
+        return lambda **kw: mxa.prefill(t["q"], t["cu"], t["k"], t["v"], t["table"], t["lens"], prepared=prep, **kw)
+    if which == "varlen":
+        wide = torch.empty(B, prepared_q, HQ, D, dtype=torch.float16, device="meta")
+        prep = mxa.prepare(wide, t["k"], t["table"], max_seqlen_k=prepared_k, device="cpu")
+        return lambda **kw: mxa.decode_varlen(t["q"], t["cu"], t["k"], t["v"], t["table"], t["lens"], prepared=prep, **kw)
+    more = dict(window=dict(window=256), float32=dict(out_dtype=torch.float32),
+                append=dict(k_new=torch.zeros(B, 1, HKV, D, dtype=torch.float16), v_new=torch.zeros(B, 1, HKV, D, dtype=torch.float16)),
+                decode={})[which]
+    prep = mxa.prepare(row_q, t["k"], t["table"], max_seqlen_k=prepared_k, window=more.get("window", 0))
+    return lambda **kw: mxa.decode(row_q, t["k"], t["v"], t["table"], t["lens"], causal=True, prepared=prep, **more, **kw)
+
+
+@pytest.mark.parametrize("which", ["prefill", "varlen", "decode", "window", "float32", "append"])
+def test_a_call_may_go_past_the_keys_it_was_prepared_for(ran, which):
+    call = bounds_call(which, tensors(), 4, 128)
+    q = dict(max_seqlen_q=4) if which in ("prefill", "varlen") else {}
+    for stated, want in ((None, 128), (64, 128), (128, 128), (700, 700), (1 << 20, WIDTH * PAGE)):
+        call(max_seqlen_k=stated, **q)
+        assert ran[-1][2].max_seqlen_k == want
+    call(**q)
+    assert ran[-1][2].max_seqlen_k == 128  # the preparation is as it was
+
+
+@pytest.mark.parametrize("which", ["prefill", "varlen"])
+def test_a_call_may_go_past_the_queries_it_was_prepared_for(ran, which):
+    call = bounds_call(which, tensors(), 4, 128)
+    for stated, want in ((1, 4), (4, 4), (200, 200), (4, 4)):
+        call(max_seqlen_q=stated)
+        assert (ran[-1][2].q_len, ran[-1][2].max_seqlen_k) == (want, 128)
+
+
+def test_a_wider_call_is_checked_against_its_plan():
+    # the library sizes the workspace anew from the widened shape
+    p = mxa.mxa_decode_params_t(4, 1, 32, 8, 128, 512, 16, 1024, 4096, mxa.MXA_BF16)
+    plan = mxa.mxa_plan(p, 0, 148)
+    wide = mxa._widened(p, 16, None)
+    assert (wide.q_len, p.q_len) == (16, 1)
+    fake = ctypes.c_void_p(4096)  # not used: the call is refused first
+    call = [fake, fake, 64, fake, fake, fake, fake, ctypes.byref(wide), 1.0, 0, ctypes.byref(plan), fake,
+            plan.workspace_bytes, fake, None, None]
+    assert mxa._lib.mxa_decode_fwd_varlen(*call) == mxa.MXA_ERR_WORKSPACE
