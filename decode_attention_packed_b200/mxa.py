@@ -140,19 +140,19 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _empty(stream, shape, dtype, device) -> torch.Tensor:
-    """torch.empty for a call on `stream` (None: the current one).  The memory
-    comes from the pool of the stream that writes it, so nothing queued on the
-    current stream still uses it and nothing allocated there gets it while the
-    call runs.  It is lent to the current stream, where the caller waits for
-    the call and reads it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+def _empty(stream, like: torch.Tensor, shape=None, dtype=None, device=None) -> torch.Tensor:
+    """A tensor as `like`, or of another shape, type and device, for a call on
+    `stream` (None: the current one).  The memory comes from the pool of the
+    stream that writes it, so nothing queued on the current stream still uses
+    it and nothing allocated there gets it while the call runs.  It is lent to
+    the current stream, where the caller waits for the call and reads it."""
+    if stream is None:  # by the calls of least host time
+        return torch.empty_like(like) if shape is None else like.new_empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         handle = _stream(stream)  # 0 and 1 name the legacy default stream
         stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = _empty(None, like, shape, dtype, device)
     t.record_stream(torch.cuda.current_stream())
     return t
 
@@ -391,7 +391,7 @@ def prepare(q, k_cache, block_table, *, max_seqlen_k=None, num_splits=0, plan=No
         plan = mxa_plan_window(params, window, sinks, num_splits) if window else mxa_plan(params, num_splits)
     ws = None
     if plan.workspace_bytes:
-        ws = _empty(stream, plan.workspace_bytes, torch.uint8, device or q.device)
+        ws = _empty(stream, q, plan.workspace_bytes, torch.uint8, device)
     return Prepared(params, plan, ws)
 
 
@@ -421,10 +421,10 @@ def decode(q, k_cache, v_cache, block_table, cache_seqlens, *, scale=None, causa
     params = _widened(prepared.params, None, max_seqlen_k)
     f32 = out_dtype == torch.float32 or (out is not None and out.dtype == torch.float32)
     if out is None:
-        out = _empty(stream, q.shape, torch.float32 if f32 else q.dtype, q.device)
+        out = _empty(stream, q, q.shape, torch.float32) if f32 else _empty(stream, q)
     if lse is None and return_lse:
         B, q_len, Hq, _ = q.shape
-        lse = _empty(stream, (B, Hq, q_len), torch.float32, q.device)
+        lse = _empty(stream, q, (B, Hq, q_len), torch.float32)
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new go together")
     if f32:
@@ -463,13 +463,13 @@ def decode_varlen(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens,
         plan = mxa_plan(params, num_splits)
         ws = None
         if plan.workspace_bytes:
-            ws = _empty(stream, plan.workspace_bytes, torch.uint8, q.device)
+            ws = _empty(stream, q, plan.workspace_bytes, torch.uint8)
         prepared = Prepared(params, plan, ws)
     params = _widened(prepared.params, max_seqlen_q, max_seqlen_k)
     if out is None:
-        out = _empty(stream, q.shape, q.dtype, q.device)
+        out = _empty(stream, q)
     if lse is None and return_lse:
-        lse = _empty(stream, (Hq, total_q), torch.float32, q.device)
+        lse = _empty(stream, q, (Hq, total_q), torch.float32)
     mxa_decode_fwd_varlen(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, params,
                           scale, causal, prepared.plan, prepared.workspace, out, lse, stream)
     return out, lse
@@ -490,7 +490,7 @@ def prepare_prefill(q, cu_seqlens_q, k_cache, block_table, *, max_seqlen_q, max_
     size = mxa_prefill_workspace_size(params, total_q)
     if size == SIZE_MAX:  # the run call names the reason
         size = 0
-    return Prepared(params, None, _empty(stream, size, torch.uint8, q.device))
+    return Prepared(params, None, _empty(stream, q, size, torch.uint8))
 
 
 def prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, max_seqlen_q, scale=None, causal=True,
@@ -523,11 +523,11 @@ def prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, ma
     if block_table is not None:
         _want(dev, block_table, "block_table", torch.int32, (B, p.max_pages_per_seq))
     if out is None:
-        out = _empty(stream, q.shape, dtype, q.device)
+        out = _empty(stream, q)
     else:
         _want(dev, out, "out", dtype, q.shape)
     if lse is None and return_lse:
-        lse = _empty(stream, (q.shape[1], q.shape[0]), torch.float32, q.device)
+        lse = _empty(stream, q, (q.shape[1], q.shape[0]), torch.float32)
     elif lse is not None:
         _want(dev, lse, "lse", torch.float32, (q.shape[1], q.shape[0]))
     mxa_prefill_fwd(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, p, scale, causal,
@@ -567,15 +567,15 @@ def extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, *, page_
     _want(dev, cu_seqlens_q, "cu_seqlens_q", int32, (B + 1,))
     _want(dev, free_pages, "free_pages", int32)
     if slots is None:
-        slots = _empty(stream, total_q, int32, block_table.device)
+        slots = _empty(stream, block_table, total_q, int32)
     else:
         _want(dev, slots, "slots", int32, (total_q,))
     if new_seqlens is None:
-        new_seqlens = _empty(stream, (B,), int32, block_table.device)
+        new_seqlens = _empty(stream, cache_seqlens)
     else:
         _want(dev, new_seqlens, "new_seqlens", int32, (B,))
     if pages_used is None:
-        pages_used = _empty(stream, 1, int32, block_table.device)
+        pages_used = _empty(stream, block_table, 1, int32)
     else:
         _want(dev, pages_used, "pages_used", int32, (1,))
     if B and new_seqlens.data_ptr() == cache_seqlens.data_ptr():

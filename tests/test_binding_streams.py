@@ -20,13 +20,14 @@ class Record:
 
     def __init__(self, monkeypatch):
         self.made, self.lent, self.inside = [], [], [None]
-        empty = torch.empty
 
-        def recording_empty(*args, **kw):
-            t = empty(*args, **kw)
-            if kw.get("device") != "meta":
-                self.made.append((t, self.inside[-1]))
-            return t
+        def recording(make):
+            def made(*args, **kw):
+                t = make(*args, **kw)
+                if kw.get("device") != "meta":
+                    self.made.append((t, self.inside[-1]))
+                return t
+            return made
 
         @contextlib.contextmanager
         def stream(s):
@@ -34,8 +35,8 @@ class Record:
             yield
             self.inside.pop()
 
-        monkeypatch.setattr(mxa.torch, "empty", recording_empty)
-        monkeypatch.setattr(mxa.torch, "empty_like", lambda t: recording_empty(t.shape, dtype=t.dtype))
+        for where, name in ((mxa.torch, "empty"), (mxa.torch, "empty_like"), (mxa.torch.Tensor, "new_empty")):
+            monkeypatch.setattr(where, name, recording(getattr(where, name)))
         monkeypatch.setattr(mxa.torch.cuda, "Stream", FakeStream)
         monkeypatch.setattr(mxa.torch.cuda, "ExternalStream", FakeStream)
         monkeypatch.setattr(mxa.torch.cuda, "default_stream", lambda: FakeStream(0))
