@@ -140,19 +140,19 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _empty(stream, like: torch.Tensor, shape=None, dtype=None, device=None) -> torch.Tensor:
-    """A tensor as `like`, or of another shape, type and device, for a call on
-    `stream` (None: the current one).  The memory comes from the pool of the
-    stream that writes it, so nothing queued on the current stream still uses
-    it and nothing allocated there gets it while the call runs.  It is lent to
-    the current stream, where the caller waits for the call and reads it."""
+def _empty(stream, like: torch.Tensor, shape=None, dtype=None) -> torch.Tensor:
+    """A tensor as `like`, or of another shape and type, for a call on `stream`
+    (None: the current one).  The memory comes from the pool of the stream that
+    writes it, so nothing queued on the current stream still uses it and nothing
+    allocated there gets it while the call runs.  It is lent to the current
+    stream, where the caller waits for the call and reads it."""
     if stream is None:  # by the calls of least host time
-        return torch.empty_like(like) if shape is None else like.new_empty(shape, dtype=dtype, device=device)
+        return torch.empty_like(like) if shape is None else like.new_empty(*shape, dtype=dtype)
     if not isinstance(stream, torch.cuda.Stream):
         handle = _stream(stream)  # 0 and 1 name the legacy default stream
         stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
-        t = _empty(None, like, shape, dtype, device)
+        t = _empty(None, like, shape, dtype)
     t.record_stream(torch.cuda.current_stream())
     return t
 
@@ -274,11 +274,16 @@ def mxa_decode_fwd_window(q, k_cache, v_cache, k_new, v_new, block_table, cache_
     """Causal decode in which the query at position p sees its last `window`
     keys and the first `sinks` keys; k_new / v_new as in
     mxa_decode_fwd_append, or None (see mxa.h)."""
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.mxa_decode_fwd_window(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_new), _ptr(v_new),
-                                      _ptr(block_table), _ptr(cache_seqlens), ctypes.byref(params), float(scale),
-                                      int(window), int(sinks), ctypes.byref(plan), _ptr(workspace), ws_bytes,
-                                      _ptr(out), _ptr(lse), _stream(stream)), "mxa_decode_fwd_window")
+    ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    code = _lib.mxa_decode_fwd_window(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                      None if k_new is None else k_new.data_ptr(),
+                                      None if v_new is None else v_new.data_ptr(),
+                                      None if block_table is None else block_table.data_ptr(),
+                                      cache_seqlens.data_ptr(), ctypes.byref(params), float(scale), int(window), int(sinks),
+                                      ctypes.byref(plan), ws, ws_bytes, out.data_ptr(),
+                                      None if lse is None else lse.data_ptr(), _stream(stream))
+    if code != MXA_OK:
+        raise MxaError(code, "mxa_decode_fwd_window")
 
 
 def mxa_prefill_workspace_size(params: mxa_decode_params_t, total_q: int) -> int:
@@ -391,7 +396,7 @@ def prepare(q, k_cache, block_table, *, max_seqlen_k=None, num_splits=0, plan=No
         plan = mxa_plan_window(params, window, sinks, num_splits) if window else mxa_plan(params, num_splits)
     ws = None
     if plan.workspace_bytes:
-        ws = _empty(stream, q, plan.workspace_bytes, torch.uint8, device)
+        ws = _empty(stream, q if device is None else torch.empty(0, device=device), (plan.workspace_bytes,), torch.uint8)
     return Prepared(params, plan, ws)
 
 
@@ -408,25 +413,32 @@ def decode(q, k_cache, v_cache, block_table, cache_seqlens, *, scale=None, causa
 
     window > 0 (causal only) leaves each query its last `window` keys and the
     first `sinks` keys of its row (mxa_decode_fwd_window); the blocks between
-    them are not read."""
+    them are not read.
+
+    All tensors are dense; a windowed call checks them against its
+    preparation, a call without a window passes them on as they are."""
     if window < 0 or sinks < 0 or (sinks and not window):
         raise ValueError("window >= 0, and sinks >= 0 go with a window")
     if window and not causal:
         raise ValueError("a sliding window is causal: pass causal=True")
-    if scale is None:
-        scale = q.shape[-1] ** -0.5
     if prepared is None:
         prepared = prepare(q, k_cache, block_table, max_seqlen_k=max_seqlen_k, num_splits=num_splits,
                            window=window, sinks=sinks, stream=stream)
-    params = _widened(prepared.params, None, max_seqlen_k)
+    params = prepared.params if max_seqlen_k is None else _widened(prepared.params, None, max_seqlen_k)
+    if scale is None:
+        scale = params.D ** -0.5
     f32 = out_dtype == torch.float32 or (out is not None and out.dtype == torch.float32)
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new go together")
+    if window and not f32:
+        _want_decode(params, q, k_cache, v_cache, block_table, cache_seqlens, prepared.workspace, out, lse, k_new, v_new)
+    elif k_new is not None and not (k_new.is_contiguous() and v_new.is_contiguous()):
+        raise ValueError("k_new and v_new must be contiguous (write_cache takes slices of a fused projection)")
     if out is None:
         out = _empty(stream, q, q.shape, torch.float32) if f32 else _empty(stream, q)
     if lse is None and return_lse:
         B, q_len, Hq, _ = q.shape
         lse = _empty(stream, q, (B, Hq, q_len), torch.float32)
-    if (k_new is None) != (v_new is None):
-        raise ValueError("k_new and v_new go together")
     if f32:
         if window:
             raise ValueError("a float32 output is not offered with a window")
@@ -463,7 +475,7 @@ def decode_varlen(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens,
         plan = mxa_plan(params, num_splits)
         ws = None
         if plan.workspace_bytes:
-            ws = _empty(stream, q, plan.workspace_bytes, torch.uint8)
+            ws = _empty(stream, q, (plan.workspace_bytes,), torch.uint8)
         prepared = Prepared(params, plan, ws)
     params = _widened(prepared.params, max_seqlen_q, max_seqlen_k)
     if out is None:
@@ -490,7 +502,7 @@ def prepare_prefill(q, cu_seqlens_q, k_cache, block_table, *, max_seqlen_q, max_
     size = mxa_prefill_workspace_size(params, total_q)
     if size == SIZE_MAX:  # the run call names the reason
         size = 0
-    return Prepared(params, None, _empty(stream, q, size, torch.uint8))
+    return Prepared(params, None, _empty(stream, q, (size,), torch.uint8))
 
 
 def prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, max_seqlen_q, scale=None, causal=True,
@@ -512,13 +524,12 @@ def prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, ma
                                    max_seqlen_k=max_seqlen_k, stream=stream)
     p, dev, dtype = _widened(prepared.params, max_seqlen_q, max_seqlen_k), _current_device(), q.dtype
     B = p.B
-    if dtype is not (torch.bfloat16 if p.dtype == MXA_BF16 else torch.float16):
-        raise TypeError("q must have the type that the call was prepared for")
+    _want_type(q, p)
     _want(dev, prepared.workspace, "the prepared workspace", torch.uint8)
     _want(dev, q, "q", dtype, (q.shape[0], p.Hq, p.D))
+    _want(dev, cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
     _want(dev, k_cache, "k_cache", dtype, (p.num_pages, p.page_size, p.Hkv, p.D))
     _want(dev, v_cache, "v_cache", dtype, k_cache.shape)
-    _want(dev, cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
     _want(dev, cache_seqlens, "cache_seqlens", torch.int32, (B,))
     if block_table is not None:
         _want(dev, block_table, "block_table", torch.int32, (B, p.max_pages_per_seq))
@@ -535,9 +546,49 @@ def prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlens, *, ma
     return out, lse
 
 
+def _want_decode(p: mxa_decode_params_t, q, k_cache, v_cache, block_table, cache_seqlens, workspace, out, lse, k_new,
+                 v_new) -> None:
+    dev, dtype, B, q_len, Hq = _current_device(), q.dtype, p.B, p.q_len, p.Hq
+    cache = (p.num_pages, p.page_size, p.Hkv, p.D)
+    # All that a call always has in one condition: a short call is bound by the
+    # host, which takes half as long for it as for the tests by name.
+    if not (dtype is k_cache.dtype is v_cache.dtype is (torch.bfloat16 if p.dtype == MXA_BF16 else torch.float16)
+            and cache_seqlens.dtype is torch.int32
+            and q.get_device() == k_cache.get_device() == v_cache.get_device() == cache_seqlens.get_device() == dev
+            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous() and cache_seqlens.is_contiguous()
+            and q.shape == (B, q_len, Hq, p.D) and k_cache.shape == cache and v_cache.shape == cache
+            and cache_seqlens.shape == (B,)
+            and (block_table is None or block_table.dtype is torch.int32 and block_table.get_device() == dev
+                 and block_table.is_contiguous() and block_table.shape == (B, p.max_pages_per_seq))
+            and (workspace is None or workspace.get_device() == dev)):
+        _want_type(q, p)
+        _want(dev, q, "q", dtype, (B, q_len, Hq, p.D))
+        _want(dev, k_cache, "k_cache", dtype, cache)
+        _want(dev, v_cache, "v_cache", dtype, cache)
+        _want(dev, cache_seqlens, "cache_seqlens", torch.int32, (B,))
+        if block_table is not None:
+            _want(dev, block_table, "block_table", torch.int32, (B, p.max_pages_per_seq))
+        if workspace is not None:
+            _want(dev, workspace, "the prepared workspace", workspace.dtype)
+    if out is not None:
+        _want(dev, out, "out", dtype, q.shape)
+    if lse is not None:
+        _want(dev, lse, "lse", torch.float32, (B, Hq, q_len))
+    if k_new is not None:
+        _want(dev, k_new, "k_new", dtype, (B, q_len, p.Hkv, p.D))
+        _want(dev, v_new, "v_new", dtype, k_new.shape)
+
+
+def _want_type(q: torch.Tensor, p: mxa_decode_params_t) -> None:
+    if q.dtype is not (torch.bfloat16 if p.dtype == MXA_BF16 else torch.float16):
+        raise TypeError("q must have the type that the call was prepared for")
+
+
 def _want(device: int, t: torch.Tensor, name: str, dtype, shape=None) -> None:
     """A dense tensor of `dtype` (and `shape`) on CUDA device `device`, the
     current one, or an error that names it."""
+    if t.dtype is dtype and t.get_device() == device and t.is_contiguous() and (shape is None or t.shape == shape):
+        return
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.get_device() != device:  # -1 for a tensor on the host
@@ -567,7 +618,7 @@ def extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, *, page_
     _want(dev, cu_seqlens_q, "cu_seqlens_q", int32, (B + 1,))
     _want(dev, free_pages, "free_pages", int32)
     if slots is None:
-        slots = _empty(stream, block_table, total_q, int32)
+        slots = _empty(stream, block_table, (total_q,), int32)
     else:
         _want(dev, slots, "slots", int32, (total_q,))
     if new_seqlens is None:
@@ -575,7 +626,7 @@ def extend_tables(block_table, cache_seqlens, cu_seqlens_q, free_pages, *, page_
     else:
         _want(dev, new_seqlens, "new_seqlens", int32, (B,))
     if pages_used is None:
-        pages_used = _empty(stream, block_table, 1, int32)
+        pages_used = _empty(stream, block_table, (1,), int32)
     else:
         _want(dev, pages_used, "pages_used", int32, (1,))
     if B and new_seqlens.data_ptr() == cache_seqlens.data_ptr():

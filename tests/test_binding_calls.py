@@ -91,3 +91,84 @@ def test_a_wider_call_is_checked_against_its_plan():
     call = [fake, fake, 64, fake, fake, fake, fake, ctypes.byref(wide), 1.0, 0, ctypes.byref(plan), fake,
             plan.workspace_bytes, fake, None, None]
     assert mxa._lib.mxa_decode_fwd_varlen(*call) == mxa.MXA_ERR_WORKSPACE
+
+
+def windowed(t, **kw):
+    """A windowed decode on `t` with replacements `kw`, prepared for the shapes of tensors()."""
+    good = tensors()
+    prep = mxa.prepare(good["q"].view(B, 1, HQ, D), good["k"], good["table"], window=256)
+    args = dict(t, **{n: kw.pop(n) for n in list(kw) if n in t})
+    return mxa.decode(args["q"], args["k"], args["v"], args["table"], args["lens"], causal=True, window=256, prepared=prep, **kw)
+
+
+def test_windowed_decode_takes_the_documented_tensors(ran):
+    t = tensors()
+    t["q"] = t["q"].view(B, 1, HQ, D)
+    fresh = torch.zeros(B, 1, HKV, D, dtype=torch.float16)
+    windowed(t)
+    windowed(t, k_new=fresh, v_new=fresh)
+    windowed(t, out=torch.zeros_like(t["q"]), lse=torch.zeros(B, HQ, 1))
+    windowed(t, q=torch.zeros(4, B, 1, HQ, D, dtype=torch.float16)[2])  # a dense part of a larger tensor
+    assert [c[0] for c in ran] == ["mxa_decode_fwd_window"] * 4
+
+
+BAD = {
+    "q of another type": (TypeError, lambda t: dict(q=t["q"].bfloat16())),
+    "q strided": (ValueError, lambda t: dict(q=torch.zeros(B, 1, 2 * HQ, D, dtype=torch.float16)[:, :, ::2])),
+    "q of more rows": (ValueError, lambda t: dict(q=torch.zeros(B + 1, 1, HQ, D, dtype=torch.float16))),
+    "q of more tokens": (ValueError, lambda t: dict(q=torch.zeros(B, 2, HQ, D, dtype=torch.float16))),
+    "another cache": (ValueError, lambda t: dict(k=t["k"][:-1], v=t["v"][:-1])),
+    "a cache of another type": (TypeError, lambda t: dict(k=t["k"].bfloat16())),
+    "values of another shape": (ValueError, lambda t: dict(v=t["v"][:-1])),
+    "a strided cache": (ValueError, lambda t: dict(k=torch.zeros(B * WIDTH, PAGE, 2 * HKV, D, dtype=torch.float16)[:, :, :HKV])),
+    "a table of another width": (ValueError, lambda t: dict(table=t["table"][:, :-1].contiguous())),
+    "a strided table": (ValueError, lambda t: dict(table=t["table"].t().contiguous().t())),
+    "a table of 64 bits": (TypeError, lambda t: dict(table=t["table"].long())),
+    "lengths of 64 bits": (TypeError, lambda t: dict(lens=t["lens"].long())),
+    "lengths of fewer rows": (ValueError, lambda t: dict(lens=t["lens"][:-1])),
+    "new keys out of a fused projection": (ValueError, lambda t: dict(k_new=fused(), v_new=fused())),
+    "new values out of a fused projection": (ValueError, lambda t: dict(k_new=fused().contiguous(), v_new=fused())),
+    "new keys of another type": (TypeError, lambda t: dict(k_new=fused().bfloat16(), v_new=fused().contiguous())),
+    "new keys of another shape": (ValueError, lambda t: dict(k_new=fused()[:1].contiguous(), v_new=fused().contiguous())),
+    "new keys alone": (ValueError, lambda t: dict(k_new=fused().contiguous())),
+    "out of another type": (TypeError, lambda t: dict(out=torch.zeros(B, 1, HQ, D, dtype=torch.bfloat16))),
+    "out of another shape": (ValueError, lambda t: dict(out=torch.zeros(B, 1, HQ + 1, D, dtype=torch.float16))),
+    "a strided out": (ValueError, lambda t: dict(out=torch.zeros(B, 1, 2 * HQ, D, dtype=torch.float16)[:, :, ::2])),
+    "an lse of 16 bits": (TypeError, lambda t: dict(lse=torch.zeros(B, HQ, 1, dtype=torch.float16))),
+    "an lse of another shape": (ValueError, lambda t: dict(lse=torch.zeros(B, HQ, 2))),
+}
+
+
+def fused():
+    return torch.zeros(B, 1, (HQ + 2 * HKV) * D, dtype=torch.float16)[:, :, HQ * D:(HQ + HKV) * D].view(B, 1, HKV, D)
+
+
+@pytest.mark.parametrize("what", sorted(BAD))
+def test_windowed_decode_refuses(ran, what):
+    error, change = BAD[what]
+    t = tensors()
+    t["q"] = t["q"].view(B, 1, HQ, D)
+    with pytest.raises(error):
+        windowed(t, **change(t))
+    assert ran == []
+
+
+def test_windowed_decode_refuses_another_device(ran, monkeypatch):
+    t = tensors()
+    t["q"] = t["q"].view(B, 1, HQ, D)
+    monkeypatch.setattr(mxa, "_current_device", lambda: 0)
+    with pytest.raises(ValueError):
+        windowed(t)
+    assert ran == []
+
+
+def test_append_refuses_strided_tokens(ran):
+    # read as dense they would be other tokens' values
+    t = tensors()
+    q = t["q"].view(B, 1, HQ, D)
+    for k_new, v_new in ((fused(), fused()), (fused().contiguous(), fused()), (fused(), fused().contiguous())):
+        with pytest.raises(ValueError):
+            mxa.decode(q, t["k"], t["v"], t["table"], t["lens"], k_new=k_new, v_new=v_new)
+    assert ran == []
+    mxa.decode(q, t["k"], t["v"], t["table"], t["lens"], k_new=fused().contiguous(), v_new=fused().contiguous())
+    assert [c[0] for c in ran] == ["mxa_decode_fwd_append"]
