@@ -261,10 +261,17 @@ def mxa_decode_fwd_noalloc(q, k_cache, v_cache, block_table, cache_seqlens, para
                                        _stream(stream)), "mxa_decode_fwd_noalloc")
 
 
+def _keys(n) -> int:
+    """A count of keys as the library takes it, in 32 bits: more than that is
+    more than any row holds, and what is negative is refused."""
+    n = int(n)
+    return n if 0 <= n <= 0x7fffffff else 0x7fffffff if n > 0 else -1
+
+
 def mxa_plan_window(params: mxa_decode_params_t, window: int, sinks: int = 0, num_splits: int = 0,
                     sm_count: int = 0) -> mxa_plan_t:
     plan = mxa_plan_t()
-    _check(_lib.mxa_plan_window(ctypes.byref(params), int(window), int(sinks), num_splits, sm_count,
+    _check(_lib.mxa_plan_window(ctypes.byref(params), _keys(window), _keys(sinks), num_splits, sm_count,
                                 ctypes.byref(plan)), "mxa_plan_window")
     return plan
 
@@ -279,7 +286,7 @@ def mxa_decode_fwd_window(q, k_cache, v_cache, k_new, v_new, block_table, cache_
                                       None if k_new is None else k_new.data_ptr(),
                                       None if v_new is None else v_new.data_ptr(),
                                       None if block_table is None else block_table.data_ptr(),
-                                      cache_seqlens.data_ptr(), ctypes.byref(params), float(scale), int(window), int(sinks),
+                                      cache_seqlens.data_ptr(), ctypes.byref(params), float(scale), _keys(window), _keys(sinks),
                                       ctypes.byref(plan), ws, ws_bytes, out.data_ptr(),
                                       None if lse is None else lse.data_ptr(), _stream(stream))
     if code != MXA_OK:
@@ -298,7 +305,7 @@ def mxa_prefill_fwd(q, cu_seqlens_q, k_cache, v_cache, block_table, cache_seqlen
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.mxa_prefill_fwd(_ptr(q), _ptr(cu_seqlens_q), q.shape[0], _ptr(k_cache), _ptr(v_cache),
                                 _ptr(block_table), _ptr(cache_seqlens), ctypes.byref(params), float(scale),
-                                int(causal), int(window), int(sinks), _ptr(workspace), ws_bytes, _ptr(out),
+                                int(causal), _keys(window), _keys(sinks), _ptr(workspace), ws_bytes, _ptr(out),
                                 _ptr(lse), _stream(stream)), "mxa_prefill_fwd")
 
 

@@ -172,3 +172,27 @@ def test_append_refuses_strided_tokens(ran):
     assert ran == []
     mxa.decode(q, t["k"], t["v"], t["table"], t["lens"], k_new=fused().contiguous(), v_new=fused().contiguous())
     assert [c[0] for c in ran] == ["mxa_decode_fwd_append"]
+
+
+@pytest.mark.parametrize("given,want", [(2**31 - 1, 2**31 - 1), (2**31, 2**31 - 1), (2**32, 2**31 - 1), (2**32 + 5, 2**31 - 1),
+                                        (2**63 - 1, 2**31 - 1), (7, 7)])
+def test_windows_past_32_bits_hide_nothing(ran, given, want):
+    # as many keys as no row has: not what 32 bits leave of the number
+    t = tensors()
+    q = t["q"].view(B, 1, HQ, D)
+    mxa.decode(q, t["k"], t["v"], t["table"], t["lens"], causal=True, window=given, sinks=given)
+    mxa.prefill(t["q"], t["cu"], t["k"], t["v"], t["table"], t["lens"], max_seqlen_q=1, window=given, sinks=given)
+    assert ran[0][1][9:11] == (want, want) and ran[1][1][10:12] == (want, want)
+    p = mxa.mxa_decode_params_t(B, 1, HQ, HKV, D, B * WIDTH, PAGE, WIDTH, WIDTH * PAGE, mxa.MXA_F16)
+    assert mxa.mxa_plan_window(p, given, given).as_dict() == mxa.mxa_plan_window(p, want, want).as_dict()
+
+
+@pytest.mark.parametrize("given", [-1, -2**31, -2**32 + 5])
+def test_negative_windows_stay_negative(ran, given):
+    t = tensors()
+    q = t["q"].view(B, 1, HQ, D)
+    for kw in (dict(window=given), dict(window=5, sinks=given)):
+        with pytest.raises(ValueError):
+            mxa.decode(q, t["k"], t["v"], t["table"], t["lens"], causal=True, **kw)
+        mxa.prefill(t["q"], t["cu"], t["k"], t["v"], t["table"], t["lens"], max_seqlen_q=1, **kw)
+        assert min(ran[-1][1][10:12]) == -1  # which the library refuses

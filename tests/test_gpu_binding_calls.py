@@ -49,3 +49,16 @@ def test_a_row_longer_than_the_decode_was_prepared_for(window, sinks, num_splits
     torch.cuda.synchronize()
     assert mxa.mxa_device_error(True) == mxa.MXA_OK
     check(inp, q, cu, out.cpu().view(q.shape), lse.cpu().view(3, -1).t(), window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("window,sinks", [(2**40 + 5, 0), (2**31 - 1, 2**40), (3, 2**32 + 1)])
+def test_windows_past_32_bits_hide_nothing(window, sinks):
+    inp, q, cu = draw([1, 1, 1], [2000, 3000, 60], seed=2330)
+    qd, cd, k, v, table, lens = [x.cuda() for x in (q, cu, inp.k_cache, inp.v_cache, inp.block_table, inp.cache_seqlens)]
+    rows = qd.view(3, 1, *q.shape[1:])
+    out, lse = mxa.decode(rows, k, v, table, lens, causal=True, window=window, sinks=sinks)
+    chunk = mxa.prefill(qd, cd, k, v, table, lens, max_seqlen_q=1, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    assert mxa.mxa_device_error(True) == mxa.MXA_OK
+    check(inp, q, cu, out.cpu().view(q.shape), lse.cpu().view(3, -1).t())
+    check(inp, q, cu, chunk[0].cpu(), chunk[1].cpu())
