@@ -401,8 +401,8 @@ mxa_status_t mxa_prefill_fwd(const void *q, const int32_t *cu_seqlens_q, int tot
   mxa_status_t st = check_prefill(p, total_q);
   if (st != MXA_OK) return st;
   if (block_table == nullptr) {
-    if (p->num_pages != p->B && p->B > 0) return MXA_ERR_INVALID_ARG;
-    if (p->page_size < p->max_seqlen_k) return MXA_ERR_INVALID_ARG;
+    // (without rows an empty block table has no address either)
+    if (p->B > 0 && (p->num_pages != p->B || p->page_size < p->max_seqlen_k)) return MXA_ERR_INVALID_ARG;
   } else {
     if ((long long)p->max_pages_per_seq * p->page_size < p->max_seqlen_k) return MXA_ERR_INVALID_ARG;
     if (p->page_size % 8 != 0) return MXA_ERR_UNSUPPORTED;

@@ -504,8 +504,9 @@ def prepare_prefill(q, cu_seqlens_q, k_cache, block_table, *, max_seqlen_q, max_
     a serving loop to keep: calls on `stream` (None: the current one)."""
     total_q, Hq, D = q.shape
     B = cu_seqlens_q.shape[0] - 1
-    shape = torch.empty((B, int(max_seqlen_q), Hq, D), dtype=q.dtype, device="meta")
+    shape = torch.empty((B, 1, Hq, D), dtype=q.dtype, device="meta")
     params = params_for(shape, k_cache, block_table, max_seqlen_k)
+    params.q_len = int(max_seqlen_q) or 1  # 0: no row has a token
     size = mxa_prefill_workspace_size(params, total_q)
     if size == SIZE_MAX:  # the run call names the reason
         size = 0

@@ -196,3 +196,25 @@ def test_negative_windows_stay_negative(ran, given):
             mxa.decode(q, t["k"], t["v"], t["table"], t["lens"], causal=True, **kw)
         mxa.prefill(t["q"], t["cu"], t["k"], t["v"], t["table"], t["lens"], max_seqlen_q=1, **kw)
         assert min(ran[-1][1][10:12]) == -1  # which the library refuses
+
+
+def test_a_step_without_new_tokens(ran):
+    # every row idle: the largest count is 0, with padding tokens or none
+    t = tensors()
+    for tokens in (0, 3):
+        mxa.prefill(t["q"][:tokens], torch.zeros_like(t["cu"]), t["k"], t["v"], t["table"], t["lens"], max_seqlen_q=0)
+        assert ran[-1][2].q_len == 1
+    prep = mxa.prepare_prefill(t["q"], t["cu"], t["k"], t["table"], max_seqlen_q=0)
+    mxa.prefill(t["q"], t["cu"], t["k"], t["v"], t["table"], t["lens"], max_seqlen_q=0, prepared=prep)
+    assert ran[-1][2].q_len == 1
+    shape = mxa.prepare_prefill(t["q"], t["cu"], t["k"], t["table"], max_seqlen_q=-1).params
+    assert shape.q_len == -1  # which the library refuses
+
+
+def test_a_step_without_rows():
+    # an empty block table has no address
+    p = mxa.mxa_decode_params_t(0, 1, HQ, HKV, D, B * WIDTH, PAGE, WIDTH, WIDTH * PAGE, mxa.MXA_F16)
+    fake = ctypes.c_void_p(4096)  # not used: there is nothing to do
+    for table in (None, fake):
+        call = [fake, fake, 0, fake, fake, table, fake, ctypes.byref(p), 1.0, 1, 0, 0, None, 0, fake, None, None]
+        assert mxa._lib.mxa_prefill_fwd(*call) == mxa.MXA_OK

@@ -62,3 +62,17 @@ def test_windows_past_32_bits_hide_nothing(window, sinks):
     assert mxa.mxa_device_error(True) == mxa.MXA_OK
     check(inp, q, cu, out.cpu().view(q.shape), lse.cpu().view(3, -1).t())
     check(inp, q, cu, chunk[0].cpu(), chunk[1].cpu())
+
+
+def test_a_step_without_new_tokens():
+    inp, q, cu = draw([4, 2], [40, 9])
+    qd, k, v, table, lens = [x.cuda() for x in (q, inp.k_cache, inp.v_cache, inp.block_table, inp.cache_seqlens)]
+    none = torch.zeros(3, dtype=torch.int32, device="cuda")
+    out, lse = mxa.prefill(qd[:0], none, k, v, table, lens, max_seqlen_q=0)
+    assert out.shape == (0, 8, 128) and lse.shape == (8, 0)
+    keep_out, keep_lse = torch.full_like(qd, 7.0), torch.full((8, 6), 7.0, device="cuda")
+    mxa.prefill(qd, none, k, v, table, lens, max_seqlen_q=0, out=keep_out, lse=keep_lse)  # padding alone
+    no_rows = mxa.prefill(qd[:0], none[:1], k, v, table[:0], lens[:0], max_seqlen_q=0)
+    torch.cuda.synchronize()
+    assert mxa.mxa_device_error(True) == mxa.MXA_OK
+    assert (keep_out == 7).all() and (keep_lse == 7).all() and no_rows[0].shape == (0, 8, 128)
