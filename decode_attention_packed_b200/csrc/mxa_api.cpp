@@ -448,9 +448,10 @@ mxa_status_t mxa_extend_tables(int32_t *block_table, const int32_t *cache_seqlen
   if (B < 0 || total_q < 0 || num_free < 0 || page_size < 1 || num_pages < 1 || max_pages_per_seq < 1)
     return MXA_ERR_INVALID_ARG;
   if (B == 0 && total_q > 0) return MXA_ERR_INVALID_ARG;
-  // slots, row capacities and the running page count are 32-bit
+  // slots, row capacities and the running page count are 32-bit; the kernel's
+  // strided loops over pages and tokens step past their ends within 32 bits
   if ((long long)num_pages * page_size > INT32_MAX || (long long)max_pages_per_seq * page_size > INT32_MAX ||
-      (long long)B * max_pages_per_seq > INT32_MAX || total_q > INT32_MAX / 2 || B > INT32_MAX / 2)
+      (long long)B * max_pages_per_seq > INT32_MAX / 2 || total_q > INT32_MAX / 2 || B > INT32_MAX / 2)
     return MXA_ERR_UNSUPPORTED;
   if (pages_used == nullptr || !aligned(pages_used, 4)) return MXA_ERR_INVALID_ARG;
   if (B > 0 && (block_table == nullptr || cache_seqlens == nullptr || cu_seqlens_q == nullptr || new_seqlens == nullptr))

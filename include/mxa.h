@@ -370,7 +370,8 @@ MXA_API size_t mxa_prefill_workspace_size(const mxa_decode_params_t *params, int
  * [0, num_pages) (slot -1) are reported by mxa_device_error as
  * MXA_ERR_INVALID_ARG.
  * Errors: MXA_ERR_INVALID_ARG (negative sizes, missing pointers, B = 0 with
- * total_q > 0), MXA_ERR_UNSUPPORTED past 32-bit sizes. */
+ * total_q > 0), MXA_ERR_UNSUPPORTED past 32-bit sizes (pool slots, a row's keys;
+ * 2^30 table entries, 2^30 tokens). */
 MXA_API mxa_status_t mxa_extend_tables(int32_t *block_table, const int32_t *cache_seqlens,
                                        const int32_t *cu_seqlens_q, const int32_t *free_pages, int B, int total_q,
                                        int num_free, int page_size, int num_pages, int max_pages_per_seq,

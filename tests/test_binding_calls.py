@@ -218,3 +218,14 @@ def test_a_step_without_rows():
     for table in (None, fake):
         call = [fake, fake, 0, fake, fake, table, fake, ctypes.byref(p), 1.0, 1, 0, 0, None, 0, fake, None, None]
         assert mxa._lib.mxa_prefill_fwd(*call) == mxa.MXA_OK
+
+
+@pytest.mark.parametrize("rows,width,code", [(2**15 + 1, 2**15, mxa.MXA_ERR_UNSUPPORTED), (2**16 - 1, 2**15, mxa.MXA_ERR_UNSUPPORTED),
+                                             (2**15, 2**15, mxa.MXA_ERR_UNSUPPORTED), (2**15 - 1, 2**15, mxa.MXA_ERR_INVALID_ARG)])
+def test_tables_stay_within_32_bits(rows, width, code):
+    # The kernel walks the pages taken, up to rows * width of them, in strides
+    # of its grid: with 2^31 - 1 pages the step past the last one would not fit
+    # 32 bits.  (The one that is small enough fails for its missing pointers.)
+    assert rows * width < 2**31
+    fake = ctypes.c_void_p(4096)  # not used: the call is refused
+    assert mxa._lib.mxa_extend_tables(None, fake, fake, fake, rows, 9, 5, 1, 64, width, fake, fake, fake, None) == code
