@@ -828,14 +828,14 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
     }
 
     // ---- the rows: O / l and LSE ----
-    const float inv = l == 0.f ? 0.f : rcp(l);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     const int hq = s.h * a.G + r_head, v0 = s.it * NT * a.TQ, tok = v0 + t * a.TQ + r_tok;
     const bool real = r_tok < a.TQ && tok < s.qn;
     // Where the row goes: row `row` of the output, or of the CTA's piece slot.
     const int row0 = s.kind == 0 ? (s.q0 + tok) * a.Hq + hq
                                  : (blockIdx.x * 2 + (s.kind - 1)) * (NT * kTileRows) + t * kTileRows + r;
     if (real) {
-      const float lse = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
+      const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       if (s.kind != 0) a.lse_part[row0] = lse;
       else if (a.lse != nullptr) a.lse[(size_t)hq * a.total_q + s.q0 + tok] = lse;
     }
