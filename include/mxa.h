@@ -364,7 +364,10 @@ MXA_API size_t mxa_prefill_workspace_size(const mxa_decode_params_t *params, int
  * A row that needs more pages than its table is wide, or than the free list
  * still holds when its turn comes, takes none: its tokens' slots are -1 and
  * new_seqlens[b] = L_b tells the caller (so does every later row that needs a
- * page once the list has run out; rows that need none go on).  Lengths
+ * page once the list has run out; rows that need none go on).  The offsets
+ * still count its n_b tokens, so an attention call of the same step takes
+ * them for the last n_b of its L_b keys: those outputs mean nothing and are
+ * the caller's to drop (n_b > 0 and new_seqlens[b] = L_b, or slot -1).  Lengths
  * outside [0, max_pages_per_seq * page_size], offsets that break their rule
  * (both clamped; the slots are then unspecified) and page ids outside
  * [0, num_pages) (slot -1) are reported by mxa_device_error as
