@@ -35,10 +35,12 @@
 // keys (64 query heads, 8 KV heads, D = 128) run at 1400 TFLOP/s for a
 // millisecond or two and at about 1200 when the card's power limit holds the
 // clock.  D = 256, per tile and 64 keys: the tensor cores 1024, measured 1800,
-// one tile's hand-overs with nothing beside them.  Tried and not kept: turns of
-// the two tiles at the exponentials, a block's scores on their way during the
-// hand-over of the weights before (slower), two groups of softmax warps that
-// take the blocks of D = 256 in turn (no change).
+// one tile's hand-overs with nothing beside them.  Tried and not kept: part of the
+// exponentials by a polynomial on the floating-point pipe (an eighth: no change;
+// a quarter: slower; measured with two threads a row, at 3000 cycles a block),
+// turns of the two tiles at the exponentials, a block's scores on their way
+// during the hand-over of the weights before (slower), two groups of softmax
+// warps that take the blocks of D = 256 in turn (no change).
 #include "mxa_config.h"
 #include "mxa_device.cuh"
 #include "mxa_launch.h"
@@ -799,8 +801,11 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
           }
         }
       }
-      // weights 2^(scale x - m), rounded to the input type, two in a word;
-      // their sum is taken before the rounding
+      // Weights 2^(scale x - m), rounded to the input type, two in a word: the
+      // tensor core takes them in the type of V.  Two words for a weight, as the
+      // decode kernel has, would double the products with V (3072 cycles instead
+      // of 2048 for a pair of tiles at D = 128, where a block takes 2650).  Their
+      // sum is taken before the rounding.
       const float base = m == -INFINITY ? 0.f : -m;
       const float2 sc = make_float2(sl2, sl2), bs = make_float2(base, base);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};

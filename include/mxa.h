@@ -277,7 +277,8 @@ MXA_API mxa_status_t mxa_decode_fwd_append(const void *q, void *k_cache, void *v
 
 /* mxa_plan for a call with a sliding window (mxa_decode_fwd_window): a row
  * streams at most the blocks of its window and its sinks, however long it is,
- * and is cut into pieces of two of them at least.  window >= 1, sinks >= 0.
+ * and with num_splits = 0 it is cut into pieces of about two of them on
+ * average (short rows and odd counts leave single ones).  window >= 1, sinks >= 0.
  * Arguments and errors otherwise as mxa_plan. */
 MXA_API mxa_status_t mxa_plan_window(const mxa_decode_params_t *params, int window, int sinks, int num_splits,
                                      int sm_count, mxa_plan_t *plan);
@@ -290,6 +291,9 @@ MXA_API mxa_status_t mxa_plan_window(const mxa_decode_params_t *params, int wind
  * that no query of the row sees are not read, and neither is a page that
  * holds such keys only (its block-table entry may hold anything), so a caller
  * may give the pages between the sinks and the window back to its pool.
+ * A key that one query of the row sees and another does not has weight 0 for
+ * the latter, and the product is taken: a NaN or an infinity among its values
+ * reaches both.  Values that no query of the row sees reach none.
  *   window : >= 1; a window of max_seqlen_k or more is plain causal attention
  *   sinks  : >= 0
  *   k_new, v_new : as in mxa_decode_fwd_append (the step's tokens are written
@@ -323,8 +327,15 @@ MXA_API mxa_status_t mxa_decode_fwd_window(const void *q, void *k_cache, void *v
  *            aligned; contents on entry are ignored; calls that may overlap
  *            need one each
  * A query that sees no key gets O = 0 and LSE = -inf.  Weights enter the
- * product with V rounded once to the input type; sums, maxima and
- * accumulators are float32.
+ * product with V rounded once to the input type, where the decode calls keep
+ * about 16 bits of them: a row of one token is more exact through
+ * mxa_decode_fwd_varlen (error against 64 bits, 2-norm, relative: bf16 2.3e-3
+ * here and 1.7e-3 there, f16 2.9e-4 and 2.1e-4).  Sums, maxima and accumulators
+ * are float32.  A key that one query sees and another of the same 128 / (Hq /
+ * Hkv) tokens (twice as many at head dims 64 and 128) does not has weight 0 for
+ * the latter, and the product is taken: a NaN or an infinity among its values
+ * reaches both.
+ * out and lse overlap none of the inputs.
  * cu_seqlens_q may end before total_q: the tokens behind the last row are
  * padding, whose out and lse are left as they were, so that one captured call
  * serves batches of up to total_q tokens and B rows (rows without tokens cost
@@ -391,7 +402,8 @@ MXA_API mxa_status_t mxa_extend_tables(int32_t *block_table, const int32_t *cach
  *                  and mxa_device_error then reports MXA_ERR_INVALID_ARG.  Slots
  *                  are distinct: a slot named twice holds 16-byte pieces of
  *                  either token.
- *   k_cache, v_cache : device [num_pages, page_size, Hkv, D] dtype
+ *   k_cache, v_cache : device [num_pages, page_size, Hkv, D] dtype; k_new and
+ *                  v_new lie outside them
  * Errors: MXA_ERR_INVALID_ARG, MXA_ERR_UNSUPPORTED for Hkv * D or a stride
  * that is not a multiple of 8 elements, or a pool past 32-bit slots. */
 MXA_API mxa_status_t mxa_cache_write(const void *k_new, const void *v_new, long long k_token_stride,
