@@ -146,10 +146,9 @@ def _empty(stream, like: torch.Tensor, shape=None, dtype=None) -> torch.Tensor:
     writes it, so nothing queued on the current stream still uses it and nothing
     allocated there gets it while the call runs.  It is lent to the current
     stream, where the caller waits for the call and reads it."""
-    if stream is None:  # by the calls of least host time
+    if stream is None or (handle := _stream(stream)) == _stream(None):  # by the calls of least host time
         return torch.empty_like(like) if shape is None else like.new_empty(*shape, dtype=dtype)
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = _stream(stream)  # 0 and 1 name the legacy default stream
+    if not isinstance(stream, torch.cuda.Stream):  # handles 0 and 1 name the legacy default stream
         stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
         t = _empty(None, like, shape, dtype)

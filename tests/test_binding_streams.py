@@ -98,3 +98,14 @@ def test_the_callers_tensors_are_left_alone(monkeypatch):
     got = mxa.prefill(q, cu, k, v, table, lens, max_seqlen_q=1, out=out, lse=lse, stream=7000)
     assert got[0] is out and got[1] is lse
     assert len(record.made) == 1 and all(t is not out and t is not lse for t, _ in record.lent)
+
+
+@pytest.mark.parametrize("stream", [FakeStream(5000), 5000])
+@pytest.mark.parametrize("which", sorted(calls()))
+def test_the_current_stream_by_name_is_none_at_all(monkeypatch, which, stream):
+    # no other stream is entered and nothing lent: the call's host time is that without stream=
+    call, count = calls()[which]
+    record = Record(monkeypatch)
+    call(stream=stream)
+    assert [at for _, at in record.made] == [None] * count and record.lent == []
+    assert record.streams == [] if which.startswith("prepare") else record.streams == [5000]
