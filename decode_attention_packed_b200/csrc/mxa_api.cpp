@@ -42,8 +42,8 @@ mxa_status_t check_shape(const mxa_decode_params_t *p) {
 mxa_status_t check_layout(const mxa_decode_params_t *p, bool contiguous) {
   const int T = block_tokens(p->D);
   if (contiguous) {
-    if (p->num_pages != p->B && p->B > 0) return MXA_ERR_INVALID_ARG;
-    if (p->page_size < p->max_seqlen_k) return MXA_ERR_INVALID_ARG;
+    // (without rows an empty block table has no address either)
+    if (p->B > 0 && (p->num_pages != p->B || p->page_size < p->max_seqlen_k)) return MXA_ERR_INVALID_ARG;
     return MXA_OK;
   }
   if ((long long)p->max_pages_per_seq * p->page_size < p->max_seqlen_k) return MXA_ERR_INVALID_ARG;

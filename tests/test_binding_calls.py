@@ -229,3 +229,14 @@ def test_tables_stay_within_32_bits(rows, width, code):
     assert rows * width < 2**31
     fake = ctypes.c_void_p(4096)  # not used: the call is refused
     assert mxa._lib.mxa_extend_tables(None, fake, fake, fake, rows, 9, 5, 1, 64, width, fake, fake, fake, None) == code
+
+
+def test_a_decode_without_rows():
+    p = mxa.mxa_decode_params_t(0, 1, HQ, HKV, D, B * WIDTH, PAGE, WIDTH, WIDTH * PAGE, mxa.MXA_F16)
+    plan = mxa.mxa_plan(p, 0, 148)
+    fake = ctypes.c_void_p(4096)  # not used: there is nothing to do
+    for table in (None, fake):
+        plain = [None, fake, fake, table, None, ctypes.byref(p), 1.0, 1, ctypes.byref(plan), None, 0, None, None, None]
+        assert mxa._lib.mxa_decode_fwd_with_plan(*plain) == mxa.MXA_OK
+        window = [None, fake, fake, None, None, table, None, ctypes.byref(p), 1.0, 5, 0, ctypes.byref(plan), None, 0, None, None, None]
+        assert mxa._lib.mxa_decode_fwd_window(*window) == mxa.MXA_OK
