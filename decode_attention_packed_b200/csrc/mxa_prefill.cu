@@ -803,9 +803,9 @@ __device__ bool softmax(const PrefillArgs &a, uint8_t *smem, uint32_t tmem, int 
       }
       // Weights 2^(scale x - m), rounded to the input type, two in a word: the
       // tensor core takes them in the type of V.  Two words for a weight, as the
-      // decode kernel has, would double the products with V (3072 cycles instead
-      // of 2048 for a pair of tiles at D = 128, where a block takes 2650).  Their
-      // sum is taken before the rounding.
+      // decode kernel has, would double the products with V (half as much again
+      // for the tensor cores, more cycles than the 2650 that a block of two tiles
+      // takes at D = 128).  Their sum is taken before the rounding.
       const float base = m == -INFINITY ? 0.f : -m;
       const float2 sc = make_float2(sl2, sl2), bs = make_float2(base, base);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
